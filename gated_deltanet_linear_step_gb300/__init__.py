@@ -24,7 +24,13 @@ from ._binding import (  # noqa: F401
     gdn_in_proj_packed,
     gdn_pack_proj_weights,
     gdn_proj_pack_bytes,
+    gdn_kv4_append,
+    gdn_kv4_attention,
+    gdn_kv4_attention_workspace_size,
+    gdn_kv4_page_bytes,
+    gdn_kv4_read,
     gdn_last_error,
+    gdn_logprobs,
     gdn_read_device_error,
     gdn_step_inputs,
     gdn_step_inputs_packed,

@@ -32,7 +32,7 @@ FLAG_GATES_READY = 0x8
 FLAG_TEST_GIVE_UP = 0x10  # tests only: the first wait for a state tile gives up (see gdn.h)
 
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_ALIGN", 4: "GDN_ERR_ALIAS",
-          5: "GDN_ERR_CUDA", 6: "GDN_ERR_FLAGS"}
+          5: "GDN_ERR_CUDA", 6: "GDN_ERR_FLAGS", 7: "GDN_ERR_DTYPE"}
 
 
 class GdnError(RuntimeError):
@@ -79,11 +79,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gdn_host_pipeline_destroy.argtypes = [_P]
         lib.gdn_host_pipeline_destroy.restype = None
         lib.gdn_in_proj_workspace_size.restype = ctypes.c_size_t
+        lib.gdn_kv4_page_bytes.argtypes = [_I] * 3
+        lib.gdn_kv4_page_bytes.restype = ctypes.c_size_t
+        lib.gdn_kv4_append.argtypes = [_P] * 6 + [_I] * 9 + [_P]
+        lib.gdn_kv4_read.argtypes = [_P] * 6 + [_I] * 9 + [_P]
+        lib.gdn_kv4_attention_workspace_size.argtypes = [_I] * 6
+        lib.gdn_kv4_attention_workspace_size.restype = ctypes.c_size_t
+        lib.gdn_kv4_attention.argtypes = [_P] * 7 + [ctypes.c_size_t] + [_I] * 10 + [ctypes.c_float, _P]
+        lib.gdn_logprobs.argtypes = [_P] * 6 + [ctypes.c_int64] * 3 + [_I, _I, _P]
         for fn in ("gdn_decode_step", "gdn_decode_step_varlen", "gdn_verify_window", "gdn_verify_commit",
                    "gdn_decode_step_ex", "gdn_ab_gates", "gdn_in_proj", "gdn_in_proj_noalloc", "gdn_step_inputs",
                    "gdn_pack_proj_weights", "gdn_in_proj_packed", "gdn_step_inputs_packed", "gdn_host_pipeline_create",
                    "gdn_host_pipeline_submit", "gdn_host_pipeline_synchronize", "gdn_get_geometry",
-                   "gdn_read_device_error"):
+                   "gdn_read_device_error", "gdn_kv4_append", "gdn_kv4_read", "gdn_kv4_attention", "gdn_logprobs"):
             getattr(lib, fn).restype = ctypes.c_int
         lib.gdn_get_geometry.argtypes = [ctypes.POINTER(ctypes.c_int32)]
         lib.gdn_read_device_error.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32)]
@@ -409,6 +417,140 @@ def gdn_step_inputs_packed(x, packed, dt, ssm_a, qkv, z, gate, beta, workspace, 
     with torch.cuda.device(dev):
         _check(lib.gdn_step_inputs_packed(_ptr(x, "x", (B, L, T, E), device=dev), pp, nbytes, *p,
                                           int(workspace.numel()), B, L, T, E, _stream_handle(stream, dev)))
+
+
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _dtype(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype not in DTYPES:
+        raise TypeError(f"{name} must be a torch.float32, torch.float16 or torch.bfloat16 tensor")
+    return DTYPES[t.dtype]
+
+
+def gdn_kv4_page_bytes(kv_heads: int, head_dim: int, page_size: int) -> int:
+    """Bytes of one page of the 4-bit key/value cache in one layer (0 for sizes out of range)."""
+    return int(load_library().gdn_kv4_page_bytes(int(kv_heads), int(head_dim), int(page_size)))
+
+
+def _kv4(cache, block_table, kv_start, seq_len, B, L, kv_heads, head_dim, page_size, dev):
+    """Checked pointers (cache, block_table, kv_start, seq_len), n_pages and max_pages of a cache call."""
+    page_bytes = gdn_kv4_page_bytes(kv_heads, head_dim, page_size)
+    if page_bytes == 0:
+        raise GdnError(2, f"kv_heads={kv_heads}, head_dim={head_dim}, page_size={page_size} are not a cache's sizes")
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
+        raise ValueError("cache must be a [L][n_pages][page_bytes] tensor")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a [B][max_pages] tensor")
+    n_pages, max_pages = int(cache.shape[1]), int(block_table.shape[1])
+    return (
+        _ptr(cache, "cache", (L, n_pages, page_bytes), dtype=torch.uint8, device=dev),
+        _ptr(block_table, "block_table", (B, max_pages), dtype=torch.int32, device=dev),
+        _ptr(kv_start, "kv_start", (B,), dtype=torch.int32, device=dev),
+        _ptr(seq_len, "seq_len", (B,), dtype=torch.int32, device=dev, optional=True),
+    ), n_pages, max_pages
+
+
+def _kv_shape(k, v):
+    if not isinstance(k, torch.Tensor) or k.dim() != 5:
+        raise ValueError("k must be a [B][L][T][kv_heads][head_dim] tensor")
+    dt = _dtype(k, "k")
+    return dt, _ptr(k, "k", k.shape, dtype=k.dtype), _ptr(v, "v", k.shape, dtype=k.dtype, device=k.device)
+
+
+def gdn_kv4_append(k, v, cache, block_table, kv_start, page_size, seq_len=None, stream=None):
+    """Quantises the window's keys and values ([B][L][T][kv_heads][head_dim], fp32, fp16 or bf16) into the
+    4-bit ``cache`` (uint8 [L][n_pages][gdn_kv4_page_bytes()]): token t of sequence b at position
+    ``kv_start[b] + t``, in page ``block_table[b][position // page_size]``. ``block_table`` is int32
+    [B][max_pages]; ``kv_start`` and the optional ``seq_len`` (valid tokens) are int32 [B]."""
+    lib = load_library()
+    dt, kp, vp = _kv_shape(k, v)
+    B, L, T, H, D = (int(n) for n in k.shape)
+    dev = k.device
+    (cp, bt, ks, sl), n_pages, max_pages = _kv4(cache, block_table, kv_start, seq_len, B, L, H, D, page_size, dev)
+    with torch.cuda.device(dev):
+        _check(lib.gdn_kv4_append(kp, vp, cp, bt, ks, sl, B, L, T, H, D, n_pages, max_pages, int(page_size), dt,
+                                  _stream_handle(stream, dev)))
+
+
+def gdn_kv4_read(cache, block_table, kv_start, k, v, page_size, seq_len=None, stream=None):
+    """Reads the cached keys and values of positions ``kv_start[b] + t`` into ``k`` and ``v`` (both
+    [B][L][T][kv_heads][head_dim]); rows at or past ``seq_len[b]`` are not written."""
+    lib = load_library()
+    dt, kp, vp = _kv_shape(k, v)
+    B, L, T, H, D = (int(n) for n in k.shape)
+    dev = k.device
+    (cp, bt, ks, sl), n_pages, max_pages = _kv4(cache, block_table, kv_start, seq_len, B, L, H, D, page_size, dev)
+    with torch.cuda.device(dev):
+        _check(lib.gdn_kv4_read(cp, bt, ks, sl, kp, vp, B, L, T, H, D, n_pages, max_pages, int(page_size), dt,
+                                _stream_handle(stream, dev)))
+
+
+def gdn_kv4_attention_workspace_size(B: int, L: int, T: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of device workspace gdn_kv4_attention needs (0 for sizes out of range)."""
+    return int(load_library().gdn_kv4_attention_workspace_size(int(B), int(L), int(T), int(q_heads), int(kv_heads),
+                                                               int(head_dim)))
+
+
+def gdn_kv4_attention(q, cache, block_table, kv_start, out, workspace, page_size, kv_heads, scale=None, seq_len=None,
+                      stream=None):
+    """Causal attention of the window's queries over the 4-bit cache: ``out`` ([B][L][T][q_heads][head_dim],
+    like ``q``) for tokens before ``seq_len[b]``; token t sees positions 0 .. ``kv_start[b] + t``, its own key
+    and value included (append them first). ``scale`` defaults to head_dim ** -0.5; ``workspace`` is a uint8
+    CUDA tensor of at least gdn_kv4_attention_workspace_size() bytes."""
+    lib = load_library()
+    if not isinstance(q, torch.Tensor) or q.dim() != 5:
+        raise ValueError("q must be a [B][L][T][q_heads][head_dim] tensor")
+    dt = _dtype(q, "q")
+    B, L, T, H, D = (int(n) for n in q.shape)
+    dev = q.device
+    if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or workspace.dim() != 1:
+        raise TypeError("workspace must be a 1-D torch.uint8 tensor")
+    qp = _ptr(q, "q", q.shape, dtype=q.dtype)
+    op = _ptr(out, "out", q.shape, dtype=q.dtype, device=dev)
+    wp = _ptr(workspace, "workspace", tuple(workspace.shape), dtype=torch.uint8, device=dev)
+    (cp, bt, ks, sl), n_pages, max_pages = _kv4(cache, block_table, kv_start, seq_len, B, L, int(kv_heads), D, page_size,
+                                                dev)
+    with torch.cuda.device(dev):
+        _check(lib.gdn_kv4_attention(qp, cp, bt, ks, sl, op, wp, int(workspace.numel()), B, L, T, H, int(kv_heads), D,
+                                     n_pages, max_pages, int(page_size), dt, D ** -0.5 if scale is None else float(scale),
+                                     _stream_handle(stream, dev)))
+
+
+def gdn_logprobs(logits, tokens=None, logprob=None, entropy=None, top_ids=None, top_logprobs=None, stream=None):
+    """From rows of logits ([N][vocab], fp32, fp16 or bf16; rows may lie further apart than vocab): the log
+    probability of ``tokens[i]`` into ``logprob`` ([N]), the entropy into ``entropy`` ([N]) and the k most
+    likely tokens into ``top_ids`` (int32 [N][k]) and ``top_logprobs`` ([N][k]), k at most 32. Outputs that
+    are None are not computed; ``tokens`` is int32 [N]."""
+    lib = load_library()
+    dt = _dtype(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be a [N][vocab] tensor")
+    if logits.device.type != "cuda":
+        raise ValueError(f"logits must be a CUDA tensor, got one on {logits.device}")
+    N, V = (int(n) for n in logits.shape)
+    ld = int(logits.stride(0)) if N > 1 else V
+    if (V > 1 and logits.stride(1) != 1) or ld < V:
+        raise ValueError("each row of logits must be contiguous, and rows may not overlap")
+    if (logprob is None) != (tokens is None):
+        raise ValueError("give both tokens and logprob, or neither")
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("give both top_ids and top_logprobs, or neither")
+    dev = logits.device
+    k = 0
+    if top_ids is not None:
+        if not isinstance(top_ids, torch.Tensor) or top_ids.dim() != 2:
+            raise ValueError("top_ids must be a [N][k] tensor")
+        k = int(top_ids.shape[1])
+    p = [
+        _ptr(tokens, "tokens", (N,), dtype=torch.int32, device=dev, optional=True),
+        _ptr(logprob, "logprob", (N,), device=dev, optional=True),
+        _ptr(entropy, "entropy", (N,), device=dev, optional=True),
+        _ptr(top_ids, "top_ids", (N, k), dtype=torch.int32, device=dev, optional=True),
+        _ptr(top_logprobs, "top_logprobs", (N, k), device=dev, optional=True),
+    ]
+    with torch.cuda.device(dev):
+        _check(lib.gdn_logprobs(logits.data_ptr(), *p, N, V, ld, k, dt, _stream_handle(stream, dev)))
 
 
 DISPATCH_KERNELS = {1: "gdn_decode_t1_kernel", 2: "gdn_window_kernel", 3: "gdn_chunk_kernel", 4: "gdn_window_tc_kernel"}

@@ -1,0 +1,853 @@
+// gdn_kv4_attention.cu - attention of a window's queries over the 4-bit cache
+// (format and pages: gdn_kv4.cuh), streaming the cache once:
+//
+//   o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  s_j = scale q . k_j,  j <= start + t
+//
+// with the running maximum m and sum of a softmax, in one pass over the keys.
+//
+// What bounds it. A cached element is 4.5 bits, so at the HBM rate an SM takes in
+// about 42 of them per clock and has about 3 issue slots of a lane for each: the
+// unpacking is what has to be cheap. One warp owns a tile of tokens; its lanes
+// unpack codes in registers in exactly the fragment order of mma.m16n8k16, with
+// the cache as the A operand and the (few) queries as the 8 columns of B: a
+// single token's query heads waste less of an 8-wide side than of a 128-row
+// tile of the tensor memory, which would also need the unpacked values written
+// to shared memory first. A code byte becomes an fp16 pair by one conversion and
+// is scaled by one multiplication; both are exact (6 significant bits).
+//
+// Fragment orders (lane = 4 g + t4). Which head dimension or token a fragment's
+// index stands for is free as long as both operands agree, so they are chosen for
+// 16-byte contiguous reads:
+//  - S^T = K Q^T: row r of an 8-row half is token kPi[r]; of a row lane t4 holds the
+//    contiguous dims 32 t4 .. (D = 128), 4 per k-step.
+//  - O^T = V^T P^T: k index pair (2 t4, 2 t4 + 1) is the token pair (kPi[2 t4], kPi[2 t4 + 1]);
+//    lane g holds the D/8 contiguous dims from g D/8 of both tokens, and interleaving
+//    the nibbles of the two tokens' words gives bytes that convert straight to the
+//    (token, next token) pairs of A. The P fragment comes from the S accumulators by movmatrix.
+//
+// Numerics. Queries are scaled by a power of two per row to fill fp16's range
+// (16-bit inputs stay exact; fp32 ones are split into fp16 hi + lo, 22 bits);
+// scores, maxima, sums and outputs are fp32. Probabilities are rounded to fp16
+// (half a step is 2^-12 of the value, below the 2^-9 of a bf16 output; 2^14 is the largest, so that small ones
+// keep their bits) or, for fp32, split into hi + lo. Masked keys take no part: their
+// scores are set to -inf by a select, and the scales of tokens past the end
+// are set to zero, so whatever such bytes hold (infinities, NaN) does not matter.
+//
+// Work split. A unit is (sequence, layer, kv head, block of query columns), its
+// tiles are cut into rounds of one tile per warp, and the rounds of all units are
+// laid end to end and dealt out evenly to the CTAs, whatever the mix of lengths.
+// A unit that crosses a CTA boundary leaves partial sums in the workspace, and a
+// second small kernel joins them in order: no atomics, so results do not
+// depend on timing.
+//
+// Waits are bounded; one that gives up stops that warp's work, sets the device error word and
+// drains the copies in flight before the CTA returns.
+
+#include <algorithm>
+#include <atomic>
+
+#include "gdn_device.cuh"
+#include "gdn_kv4.cuh"
+#include "gdn_tc.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kAttnThreads = 32 * kWarps;
+constexpr int kStages = 4;
+constexpr uint32_t kCodeBytes = 2048;   // a tile's K (or V) codes: 4096 / D tokens
+constexpr uint32_t kScaleBytes = 256;   // and their scales
+constexpr uint32_t kStageBytes = 2 * (kCodeBytes + kScaleBytes);
+constexpr float kPShift = 14.0f;        // the largest probability is 2^14
+
+__device__ unsigned int g_kv4_attn_error = 0;
+
+template <int D>
+struct Tile {
+    static constexpr int kTokens = 4096 / D;
+    static constexpr int kRow = D / 2;      // code bytes of a token
+    static constexpr int kBlocks = D / 16;  // scales of a token
+};
+
+struct AttnParams {
+    Kv4Cache c;
+    const void* q;
+    void* out;
+    float* part;  // per CTA two partial results: [columns][D] sums, then maxima and sums of the columns
+    int q_heads, group, col_blocks;
+    DType dtype;
+    float scale_log2;
+};
+
+// Token of row r of an 8-row half tile.
+__device__ __forceinline__ int pi8(int r) { return r ^ ((r >> 1) & 1); }
+
+// ------------------------------------------------------------ work split --
+// Rounds of one unit of sequence b.
+template <int D>
+__device__ __forceinline__ int seq_rounds(const Kv4Cache& c, int b) {
+    const Kv4Window w = kv4_window(c, b);
+    if (w.n == 0) return 0;
+    const int end = min(w.start + min(w.n, w.cap - w.start), w.cap);
+    constexpr int kRound = Tile<D>::kTokens * kWarps;
+    return (end + kRound - 1) / kRound;
+}
+
+struct Cursor {
+    int b, u, r, rounds;
+    long long left;  // rounds still to do in this CTA, this one included
+};
+
+// Rounds [lo, hi) of CTA i of n.
+__device__ __forceinline__ void cta_range(long long total, int i, int n, long long& lo, long long& hi) {
+    lo = total * i / n;
+    hi = total * (i + 1) / n;
+}
+
+// Sum of the sequences' rounds, by one warp.
+template <int D>
+__device__ __forceinline__ long long all_rounds(const Kv4Cache& c, int lane) {
+    long long s = 0;
+    for (int b = lane; b < c.B; b += 32) s += seq_rounds<D>(c, b);
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    return s;
+}
+
+// The unit and round that global round `at` belongs to (units per sequence: `units`), by one warp.
+template <int D>
+__device__ __forceinline__ Cursor locate(const Kv4Cache& c, int units, long long at, int lane) {
+    Cursor k;
+    k.b = c.B;
+    k.u = k.r = k.rounds = 0;
+    k.left = 0;
+    long long before = 0;
+    for (int b0 = 0; b0 < c.B; b0 += 32) {
+        const int mine = b0 + lane < c.B ? seq_rounds<D>(c, b0 + lane) : 0;
+        int sum = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += v;
+        }
+        const unsigned hit = __ballot_sync(~0u, (before + sum) * units > at);
+        if (hit != 0) {
+            const int src = __ffs(hit) - 1;
+            k.b = b0 + src;
+            k.rounds = __shfl_sync(~0u, mine, src);
+            const long long base = (before + __shfl_sync(~0u, sum, src) - k.rounds) * units;
+            k.u = static_cast<int>((at - base) / k.rounds);
+            k.r = static_cast<int>((at - base) - static_cast<long long>(k.u) * k.rounds);
+            return k;
+        }
+        before += __shfl_sync(~0u, sum, 31);
+    }
+    return k;
+}
+
+template <int D>
+__device__ __forceinline__ void advance(const Kv4Cache& c, int units, Cursor& k) {
+    --k.left;
+    if (++k.r < k.rounds) return;
+    k.r = 0;
+    if (++k.u < units) return;
+    k.u = 0;
+    do {
+        ++k.b;
+    } while (k.b < c.B && (k.rounds = seq_rounds<D>(c, k.b)) == 0);
+}
+
+// A unit: its layer, kv head, first column, and the positions its columns see.
+struct Unit {
+    int l, h, col0, start, n, end;  // end: first position that no column sees
+};
+
+__device__ __forceinline__ Unit unit_of(const AttnParams& p, int b, int u, int columns) {
+    Unit x;
+    const int qb = u % p.col_blocks;
+    const int lh = u / p.col_blocks;
+    x.h = lh % p.c.kv_heads;
+    x.l = lh / p.c.kv_heads;
+    x.col0 = qb * columns;
+    const Kv4Window w = kv4_window(p.c, b);
+    x.start = w.start;
+    x.n = w.n;
+    const int t_lo = x.col0 / p.group;
+    const int t_hi = min((x.col0 + columns - 1) / p.group, w.n - 1);
+    x.end = t_lo < w.n ? w.start + min(t_hi + 1, w.cap - w.start) : 0;
+    return x;
+}
+
+// ---------------------------------------------------------------- pieces --
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// The 8 codes of a word as four fp16 pairs, times a pair of scales.
+__device__ __forceinline__ void unpack(uint32_t w, uint32_t s, uint32_t (&v)[4]) {
+    asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+        "mov.b32 {c0, c1, c2, c3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, c0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, c1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, c3;\n\t}"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(s));
+}
+
+// Scale byte i (0 or 1) of a 16-bit pair of them, as both halves of an fp16 pair.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t two, int i) {
+    const uint32_t s = ((two >> (8 * i)) & 255u) << 7;
+    return s | (s << 16);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// What rounding to fp16 left of two floats, rounded to fp16.
+__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return pack_half2(a - f.x, b - f.y);
+}
+
+__device__ __forceinline__ float4 load_q4(const AttnParams& p, size_t i) {
+    if (p.dtype == DType::kF32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + i);
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + i);
+    if (p.dtype == DType::kF16) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void store_out2(const AttnParams& p, size_t i, float a, float b) {
+    if (p.dtype == DType::kF32) {
+        *reinterpret_cast<float2*>(static_cast<float*>(p.out) + i) = make_float2(a, b);
+    } else if (p.dtype == DType::kF16) {
+        *reinterpret_cast<uint32_t*>(static_cast<__half*>(p.out) + i) = pack_half2(a, b);
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + i) = *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
+
+// Row (t, query head) of column col of a unit: its first element in q and out.
+__device__ __forceinline__ size_t q_row(const AttnParams& p, int b, const Unit& x, int col) {
+    const int t = col / p.group;
+    const int head = x.h * p.group + (col - t * p.group);
+    return (((static_cast<size_t>(b) * p.c.L + x.l) * p.c.T + t) * p.q_heads + head) * p.c.head_dim;
+}
+
+// Output sums lie permuted: pair (i, g) of the dims (D/8) g + 2 i + {0, 1} is at 16 i + 2 g.
+template <int D>
+__device__ __forceinline__ int dim_of(int pos) {
+    return (D / 8) * ((pos >> 1) & 7) + 2 * (pos >> 4) + (pos & 1);
+}
+
+// ---------------------------------------------------------------- kernel --
+template <int D, int NT, bool SPLIT>
+struct Smem {
+    static constexpr int kCols = 8 * NT;
+    static constexpr uint32_t kRedStride = D + 8;  // floats: bank spread of the lanes' pairs
+    static constexpr uint32_t kQBytes = kCols * D * 2 * (SPLIT ? 2 : 1);
+    static constexpr uint32_t kOffQ = kWarps * kStages * kStageBytes;
+    static constexpr uint32_t kOffRed = kOffQ + kQBytes;
+    static constexpr uint32_t kOffCol = kOffRed + kWarps * 8 * kRedStride * 4;  // maxima and sums: [warp][col] twice
+    static constexpr uint32_t kOffMul = kOffCol + 2 * kWarps * kCols * 4;     // per column: scale of the raw scores
+    static constexpr uint32_t kOffBad = kOffMul + kCols * 4;                  // per stage: pages that are not there
+    static constexpr uint32_t kOffBar = kOffBad + kWarps * kStages * 4;
+    static constexpr uint32_t kBytes = kOffBar + kWarps * kStages * 8;
+};
+
+template <int D, int NT, bool SPLIT>
+__global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __grid_constant__ AttnParams p) {
+    using S = Smem<D, NT, SPLIT>;
+    using TL = Tile<D>;
+    constexpr int kCols = S::kCols;
+    constexpr int kTokens = TL::kTokens, kHalfTiles = kTokens / 16;  // m16 tiles of a tile
+    constexpr int kMTiles = D / 16;
+    extern __shared__ __align__(128) unsigned char sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    float* red = reinterpret_cast<float*>(sm + S::kOffRed);
+    float* col_m = reinterpret_cast<float*>(sm + S::kOffCol);
+    float* col_l = col_m + kWarps * kCols;
+    float* mul_s = reinterpret_cast<float*>(sm + S::kOffMul);
+    uint32_t* bad_s = reinterpret_cast<uint32_t*>(sm + S::kOffBad) + warp * kStages;
+    const uint32_t bars = smem_addr(sm + S::kOffBar) + warp * kStages * 8;
+    unsigned char* ring = sm + warp * kStages * kStageBytes;
+    const uint32_t ring_addr = smem_addr(ring);
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+
+    const int units = p.c.L * p.c.kv_heads * p.col_blocks;
+    const long long total = all_rounds<D>(p.c, lane) * units;
+    long long lo, hi;
+    cta_range(total, blockIdx.x, gridDim.x, lo, hi);
+    if (lo == hi) return;
+    Cursor cur = locate<D>(p.c, units, lo, lane);
+    cur.left = hi - lo;
+
+    const int psize = 1 << p.c.page_shift;
+    const int piece_rows = min(psize, kTokens);
+    const int piece_shift = min(p.c.page_shift, 31 - __clz(kTokens));
+    const int n_pieces = 4 * (kTokens / piece_rows);
+    bool failed = false;
+    uint32_t issued = 0, used = 0;  // this warp's tiles
+    Cursor ahead = cur;
+    Unit au = unit_of(p, ahead.b, ahead.u, kCols);
+
+    // Requests the next tile of this warp (skipping rounds in which it has none).
+    auto issue = [&]() {
+        while (ahead.left > 0) {
+            const int p0 = (ahead.r * kWarps + warp) * kTokens;
+            const bool have = p0 < au.end;
+            const int b = ahead.b, l = au.l, h = au.h, end = au.end;
+            const int old_b = ahead.b, old_u = ahead.u;
+            advance<D>(p.c, units, ahead);
+            if (ahead.left > 0 && (ahead.b != old_b || ahead.u != old_u)) au = unit_of(p, ahead.b, ahead.u, kCols);
+            if (!have) continue;
+            const uint32_t s = issued % kStages;
+            const int j = lane >> 2, kind = lane & 3;  // piece: page j of the tile; K codes, K scales, V codes, V scales
+            const int pos = p0 + j * piece_rows;
+            const bool want = lane < n_pieces && pos < end;
+            const int page = want ? kv4_page(p.c, b, pos) : -1;
+            const bool ok = page >= 0;
+            const unsigned there = __ballot_sync(~0u, ok);
+            const unsigned wanted = __ballot_sync(~0u, want);
+            if (lane == 0) {
+                bad_s[s] = there ^ wanted;
+                mbar_arrive_expect_tx(bars + 8 * s, __popc(there) / 4 * 2 * piece_rows * (TL::kRow + TL::kBlocks));
+            }
+            __syncwarp();
+            if (ok) {
+                const int row = pos & (psize - 1);
+                const uint8_t* src = p.c.cache + kv4_head_offset(p.c, l, page, h) +
+                                     ((kind & 2) ? kv4_head_bytes(psize, D) / 2 : 0);
+                uint32_t dst = ring_addr + s * kStageBytes;
+                if (kind & 1)
+                    bulk_load(dst + 2 * kCodeBytes + (kind >> 1) * kScaleBytes + j * piece_rows * TL::kBlocks,
+                              src + psize * TL::kRow + row * TL::kBlocks, piece_rows * TL::kBlocks, bars + 8 * s);
+                else
+                    bulk_load(dst + (kind >> 1) * kCodeBytes + j * piece_rows * TL::kRow, src + row * TL::kRow,
+                              piece_rows * TL::kRow, bars + 8 * s);
+            }
+            ++issued;
+            return;
+        }
+    };
+    for (int s = 0; s < kStages; ++s) issue();
+
+    while (cur.left > 0) {
+        const Unit x = unit_of(p, cur.b, cur.u, kCols);
+        const int b = cur.b;
+        const int r0 = cur.r;
+        const int r1 = static_cast<int>(min(static_cast<long long>(cur.rounds), r0 + cur.left));
+
+        // --- queries of the unit: B fragments in shared memory
+        __syncthreads();
+        const int all_cols = min(x.n * p.group - x.col0, kCols);  // columns that exist (<= 0: none)
+        if (tid == 0 && x.n > kv4_window(p.c, b).cap - x.start) atomicOr(&g_kv4_attn_error, kErrBadPage);
+        for (int c = warp; c < kCols; c += kWarps) {
+            constexpr int kChunks = D > 128 ? D / 128 : 1;
+            float4 v[kChunks];
+            float a = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (c < all_cols && 4 * lane + 128 * i < D) v[i] = load_q4(p, q_row(p, b, x, x.col0 + c) + 128 * i + 4 * lane);
+                a = fmaxf(fmaxf(a, fmaxf(fabsf(v[i].x), fabsf(v[i].y))), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
+            // f = 2^(11 - exponent of the largest magnitude): the row fills fp16's range, exactly
+            const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -115), 127);
+            const float f = a > 0.0f && a <= 3.0e38f ? __uint_as_float(static_cast<uint32_t>(138 - e) << 23) : 1.0f;
+            if (lane == 0) mul_s[c] = p.scale_log2 / f;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                if (4 * lane + 128 * i >= D) continue;
+                constexpr int kPerT4 = D >= 128 ? 8 : 4;  // k-steps of a lane's contiguous dims
+                const int st = 8 * i + (lane & (kPerT4 - 1)), tt = lane / kPerT4;
+                const float q0 = v[i].x * f, q1 = v[i].y * f, q2 = v[i].z * f, q3 = v[i].w * f;
+                const uint32_t at = ((st * NT + (c >> 3)) * 32 + (c & 7) * 4 + tt) * 8;
+                uint2 w = make_uint2(pack_half2(q0, q1), pack_half2(q2, q3));
+                *reinterpret_cast<uint2*>(sm + S::kOffQ + at) = w;
+                if constexpr (SPLIT)
+                    *reinterpret_cast<uint2*>(sm + S::kOffQ + kCols * D * 2 + at) =
+                        make_uint2(pack_rest(q0, q1, w.x), pack_rest(q2, q3, w.y));
+            }
+        }
+        __syncthreads();
+
+        float m[NT][2], ls[NT][2], mul[NT][2];
+        int lim[NT][2];  // last position that the column sees
+        float o[kMTiles][NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = 8 * nt + 2 * t4 + j;
+                m[nt][j] = -INFINITY;
+                ls[nt][j] = 0.0f;
+                mul[nt][j] = mul_s[c];
+                lim[nt][j] = c < all_cols ? min(x.start + (x.col0 + c) / p.group, x.end - 1) : -1;
+            }
+#pragma unroll
+        for (int i = 0; i < kMTiles; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
+        // positions below this are seen by every column of the block
+        const int seen_by_all = all_cols == kCols ? min(x.start + x.col0 / p.group + 1, x.end) : 0;
+
+        for (int r = r0; r < r1; ++r) {
+            const int p0 = (r * kWarps + warp) * kTokens;
+            if (p0 >= x.end || failed) continue;
+            const uint32_t s = used % kStages;
+            if (!mbar_wait_bounded(bars + 8 * s, (used / kStages) & 1u)) {
+                failed = true;
+                continue;
+            }
+            const unsigned char* st = ring + s * kStageBytes;
+            const uint32_t bad = bad_s[s];
+            const bool whole = p0 + kTokens <= seen_by_all && bad == 0;
+
+            // --- S^T = K Q^T
+            float sc[kHalfTiles][NT][4];
+#pragma unroll
+            for (int mt = 0; mt < kHalfTiles; ++mt) {
+                const int ra = 16 * mt + pi8(g), rb = ra + 8;
+                const uint8_t* ka = st + ra * TL::kRow;
+                const uint8_t* kb = st + rb * TL::kRow;
+                const uint8_t* sa = st + 2 * kCodeBytes + ra * TL::kBlocks;
+                const uint8_t* sb = st + 2 * kCodeBytes + rb * TL::kBlocks;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sc[mt][nt][j] = 0.0f;
+                constexpr int kHalves = D > 128 ? D / 128 : 1;
+#pragma unroll
+                for (int hf = 0; hf < kHalves; ++hf) {
+                    constexpr int kWords = D >= 128 ? 4 : 2;
+                    uint32_t wa[kWords], wb[kWords];
+                    uint32_t da, db;  // scale bytes of the lane's blocks
+                    if constexpr (D >= 128) {
+                        const int blk = 8 * hf + 2 * t4;
+                        const uint4 va = *reinterpret_cast<const uint4*>(ka + (blk ^ kv4_swizzle(ra, TL::kBlocks)) * 8);
+                        const uint4 vb = *reinterpret_cast<const uint4*>(kb + (blk ^ kv4_swizzle(rb, TL::kBlocks)) * 8);
+                        wa[0] = va.x, wa[1] = va.y, wa[2] = va.z, wa[3] = va.w;
+                        wb[0] = vb.x, wb[1] = vb.y, wb[2] = vb.z, wb[3] = vb.w;
+                        da = *reinterpret_cast<const uint16_t*>(sa + blk);
+                        db = *reinterpret_cast<const uint16_t*>(sb + blk);
+                    } else {
+                        const uint2 va = *reinterpret_cast<const uint2*>(ka + t4 * 8);
+                        const uint2 vb = *reinterpret_cast<const uint2*>(kb + t4 * 8);
+                        wa[0] = va.x, wa[1] = va.y;
+                        wb[0] = vb.x, wb[1] = vb.y;
+                        da = sa[t4];
+                        db = sb[t4];
+                    }
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) {
+                        uint32_t a[4], c[4];
+                        unpack(wa[w], scale_pair(da, w >> 1), a);
+                        unpack(wb[w], scale_pair(db, w >> 1), c);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int step = 8 * hf + 2 * w + k;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint32_t at = ((step * NT + nt) * 32 + lane) * 8;
+                                const uint2 qh = *reinterpret_cast<const uint2*>(sm + S::kOffQ + at);
+                                mma_f16(sc[mt][nt], a[2 * k], c[2 * k], a[2 * k + 1], c[2 * k + 1], qh.x, qh.y);
+                                if constexpr (SPLIT) {
+                                    const uint2 ql = *reinterpret_cast<const uint2*>(sm + S::kOffQ + kCols * D * 2 + at);
+                                    mma_f16(sc[mt][nt], a[2 * k], c[2 * k], a[2 * k + 1], c[2 * k + 1], ql.x, ql.y);
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+
+            // --- running maximum, probabilities
+            float nm[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                nm[nt][0] = m[nt][0];
+                nm[nt][1] = m[nt][1];
+#pragma unroll
+                for (int mt = 0; mt < kHalfTiles; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float v = sc[mt][nt][j] * mul[nt][j & 1];
+                        if (!whole) {
+                            const int row = 16 * mt + pi8(g) + 8 * (j >> 1);
+                            const bool gone = (bad >> (4 * (row >> piece_shift))) & 1u;
+                            if (p0 + row > lim[nt][j & 1] || gone) v = -INFINITY;
+                        }
+                        sc[mt][nt][j] = v;
+                        nm[nt][j & 1] = fmaxf(nm[nt][j & 1], v);
+                    }
+            }
+            bool moved = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                    for (int q = 4; q < 32; q <<= 1) nm[nt][j] = fmaxf(nm[nt][j], __shfl_xor_sync(~0u, nm[nt][j], q));
+                    moved = moved || nm[nt][j] != m[nt][j];
+                }
+            if (__any_sync(~0u, moved)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float al[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        al[j] = nm[nt][j] == m[nt][j] ? 1.0f : exp2_approx(m[nt][j] - nm[nt][j]);
+                        m[nt][j] = nm[nt][j];
+                        ls[nt][j] *= al[j];
+                    }
+#pragma unroll
+                    for (int i = 0; i < kMTiles; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[i][nt][j] *= al[j & 1];
+                }
+            }
+            uint32_t ph[kHalfTiles][NT][2], pl[kHalfTiles][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float s0 = m[nt][0] == -INFINITY ? 0.0f : kPShift - m[nt][0];
+                const float s1 = m[nt][1] == -INFINITY ? 0.0f : kPShift - m[nt][1];
+#pragma unroll
+                for (int mt = 0; mt < kHalfTiles; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const float e0 = exp2_approx(sc[mt][nt][2 * hf] + s0);
+                        const float e1 = exp2_approx(sc[mt][nt][2 * hf + 1] + s1);
+                        ls[nt][0] += e0;
+                        ls[nt][1] += e1;
+                        const uint32_t w = pack_half2(e0, e1);
+                        ph[mt][nt][hf] = transpose8(w);
+                        if constexpr (SPLIT) pl[mt][nt][hf] = transpose8(pack_rest(e0, e1, w));
+                    }
+            }
+
+            // --- O^T += V^T P^T
+#pragma unroll
+            for (int mt = 0; mt < kHalfTiles; ++mt) {
+                // the lane's four tokens: k indices 2 t4, 2 t4 + 1, and both + 8
+                const int row[4] = {16 * mt + pi8(2 * t4), 16 * mt + pi8(2 * t4 + 1), 16 * mt + 8 + pi8(2 * t4),
+                                    16 * mt + 8 + pi8(2 * t4 + 1)};
+                constexpr int kWords = D / 64;  // words of a lane's D/8 dims
+                uint32_t w[4][kWords];
+                uint32_t sb[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint8_t* v = st + kCodeBytes + row[k] * TL::kRow;
+                    const uint8_t* sv = st + 2 * kCodeBytes + kScaleBytes + row[k] * TL::kBlocks;
+                    if constexpr (D == 256) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(v + ((2 * g) ^ kv4_swizzle(row[k], TL::kBlocks)) * 8);
+                        w[k][0] = u.x, w[k][1] = u.y, w[k][2] = u.z, w[k][3] = u.w;
+                        sb[k] = *reinterpret_cast<const uint16_t*>(sv + 2 * g);
+                    } else if constexpr (D == 128) {
+                        const uint2 u = *reinterpret_cast<const uint2*>(v + (g ^ kv4_swizzle(row[k], TL::kBlocks)) * 8);
+                        w[k][0] = u.x, w[k][1] = u.y;
+                        sb[k] = sv[g];
+                    } else {
+                        w[k][0] = *reinterpret_cast<const uint32_t*>(v + g * 4);
+                        sb[k] = sv[g >> 1];
+                    }
+                    if (!whole) {
+                        const bool gone = (bad >> (4 * (row[k] >> piece_shift))) & 1u;
+                        if (p0 + row[k] >= x.end || gone) sb[k] = 0;
+                    }
+                }
+                uint32_t s01 = 0, s23 = 0;
+#pragma unroll
+                for (int wi = 0; wi < kWords; ++wi) {
+                    if (wi == 0 || wi == 2) {
+                        const int sh = 8 * (wi / 2);
+                        s01 = ((sb[0] >> sh) & 255u) << 7 | ((sb[1] >> sh) & 255u) << 23;
+                        s23 = ((sb[2] >> sh) & 255u) << 7 | ((sb[3] >> sh) & 255u) << 23;
+                    }
+                    uint32_t e01[4], o01[4], e23[4], o23[4];
+                    unpack((w[0][wi] & 0x0F0F0F0Fu) | ((w[1][wi] << 4) & 0xF0F0F0F0u), s01, e01);
+                    unpack(((w[0][wi] >> 4) & 0x0F0F0F0Fu) | (w[1][wi] & 0xF0F0F0F0u), s01, o01);
+                    unpack((w[2][wi] & 0x0F0F0F0Fu) | ((w[3][wi] << 4) & 0xF0F0F0F0u), s23, e23);
+                    unpack(((w[2][wi] >> 4) & 0x0F0F0F0Fu) | (w[3][wi] & 0xF0F0F0F0u), s23, o23);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(o[4 * wi + i][nt], e01[i], o01[i], e23[i], o23[i], ph[mt][nt][0], ph[mt][nt][1]);
+                            if constexpr (SPLIT)
+                                mma_f16(o[4 * wi + i][nt], e01[i], o01[i], e23[i], o23[i], pl[mt][nt][0], pl[mt][nt][1]);
+                        }
+                }
+            }
+            if (bad != 0 && lane == 0) atomicOr(&g_kv4_attn_error, kErrBadPage);
+            ++used;
+            __syncwarp();  // every lane has read the stage
+            issue();
+        }
+
+        // --- join the warps
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int q = 4; q < 32; q <<= 1) ls[nt][j] += __shfl_xor_sync(~0u, ls[nt][j], q);
+                if (g == 0) {
+                    col_m[warp * kCols + 8 * nt + 2 * t4 + j] = m[nt][j];
+                    col_l[warp * kCols + 8 * nt + 2 * t4 + j] = ls[nt][j];
+                }
+            }
+        __syncthreads();
+        const bool done = r0 == 0 && r1 == cur.rounds;
+        float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kCols * (D + 2));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = 8 * nt + 2 * t4 + j;
+                float mm = col_m[c];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, col_m[w * kCols + c]);
+                f[j] = m[nt][j] == -INFINITY ? 0.0f : exp2_approx(m[nt][j] - mm);
+            }
+            float* mine = red + warp * 8 * S::kRedStride + 2 * t4 * S::kRedStride + 2 * g;
+#pragma unroll
+            for (int i = 0; i < kMTiles; ++i) {
+                *reinterpret_cast<float2*>(mine + 16 * i) = make_float2(o[i][nt][0] * f[0], o[i][nt][2] * f[0]);
+                *reinterpret_cast<float2*>(mine + S::kRedStride + 16 * i) = make_float2(o[i][nt][1] * f[1], o[i][nt][3] * f[1]);
+            }
+            __syncthreads();
+            for (int e = tid; e < 8 * D / 2; e += kAttnThreads) {
+                const int c8 = e / (D / 2), pos = 2 * (e % (D / 2)), c = 8 * nt + c8;
+                if (c >= all_cols) continue;
+                float2 v = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 y = *reinterpret_cast<const float2*>(red + (w * 8 + c8) * S::kRedStride + pos);
+                    v.x += y.x;
+                    v.y += y.y;
+                }
+                float mm = col_m[c];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, col_m[w * kCols + c]);
+                float l = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float mw = col_m[w * kCols + c];
+                    l += col_l[w * kCols + c] * (mw == -INFINITY ? 0.0f : exp2_approx(mw - mm));
+                }
+                if (done) {
+                    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // no key at all: zeros
+                    store_out2(p, q_row(p, b, x, x.col0 + c) + dim_of<D>(pos), v.x * inv, v.y * inv);
+                } else {
+                    *reinterpret_cast<float2*>(slot + c * D + pos) = v;
+                    if (pos == 0) {
+                        slot[kCols * D + c] = mm;
+                        slot[kCols * D + kCols + c] = l;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+
+        // --- the next unit
+        cur.r = r1 - 1;
+        cur.left -= r1 - r0 - 1;
+        advance<D>(p.c, units, cur);
+    }
+    if (failed) {
+        if (lane == 0) atomicOr(&g_kv4_attn_error, kErrWaitTimeout);
+        while (used < issued) {
+            mbar_wait_bounded(bars + 8 * (used % kStages), (used / kStages) & 1u);
+            ++used;
+        }
+    }
+}
+
+// Joins the partial results of the units that several CTAs shared, one column per block.
+template <int D, int NT>
+__global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int kCols = 8 * NT;
+    constexpr size_t kSlot = kCols * (D + 2);
+    __shared__ float2 sums[128];
+    __shared__ float lsum[128];
+    const int lane = threadIdx.x & 31, c = blockIdx.y, n = gridDim.x;
+    const int units = p.c.L * p.c.kv_heads * p.col_blocks;
+    const long long total = all_rounds<D>(p.c, lane) * units;
+    long long lo, hi;
+    cta_range(total, blockIdx.x, n, lo, hi);
+    griddep_wait();
+    if (lo == hi) return;
+    // the unit that this CTA's last round belongs to, if it starts here and ends elsewhere
+    Cursor k = locate<D>(p.c, units, hi - 1, lane);
+    const long long first = hi - 1 - k.r, end = first + k.rounds;
+    if (first < lo || end <= hi) return;
+    const Unit x = unit_of(p, k.b, k.u, kCols);
+    if (c >= min(x.n * p.group - x.col0, kCols)) return;
+    int last = blockIdx.x;
+    while (hi < end) {
+        ++last;
+        cta_range(total, last, n, lo, hi);
+    }
+    const int parts = last - static_cast<int>(blockIdx.x) + 1;
+    const float* base = p.part + static_cast<size_t>(blockIdx.x) * 2 * kSlot;
+    auto slot = [&](int i) -> const float* { return i == 0 ? base + kSlot : base + static_cast<size_t>(i) * 2 * kSlot; };
+    auto empty = [&](int i) -> bool {
+        long long a, z;
+        cta_range(total, blockIdx.x + i, n, a, z);
+        return a == z;
+    };
+    float mm = -INFINITY;
+    for (int i = lane; i < parts; i += 32)
+        if (!empty(i)) mm = fmaxf(mm, slot(i)[kCols * D + c]);
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
+    constexpr int kPairs = D / 2, kWays = 128 / kPairs;
+    const int pair = threadIdx.x % kPairs, way = threadIdx.x / kPairs;
+    float2 v = make_float2(0.0f, 0.0f);
+    float l = 0.0f;
+    for (int i = way; i < parts; i += kWays) {
+        if (empty(i)) continue;
+        const float* s = slot(i);
+        const float ms = s[kCols * D + c];
+        const float f = ms == -INFINITY ? 0.0f : exp2_approx(ms - mm);
+        const float2 y = *reinterpret_cast<const float2*>(s + c * D + 2 * pair);
+        v.x += y.x * f;
+        v.y += y.y * f;
+        l += s[kCols * D + kCols + c] * f;
+    }
+    sums[threadIdx.x] = v;
+    lsum[threadIdx.x] = l;
+    __syncthreads();
+    if (way != 0) return;
+    for (int w = 1; w < kWays; ++w) {
+        v.x += sums[w * kPairs + pair].x;
+        v.y += sums[w * kPairs + pair].y;
+        l += lsum[w * kPairs + pair];
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    store_out2(p, q_row(p, k.b, x, x.col0 + c) + dim_of<D>(2 * pair), v.x * inv, v.y * inv);
+}
+
+// 8-column tiles per block: as few as hold the window's columns, at most 4 (2 at D = 256), where
+// the accumulators end.
+int column_tiles(int T, int group, int head_dim) {
+    const long long cols = static_cast<long long>(T) * group;
+    const int most = head_dim == 256 ? 2 : 4;
+    if (cols <= 8) return 1;
+    if (cols <= 16 || most == 2) return 2;
+    return 4;
+}
+
+constexpr int kMaxCtas = 2 * 192;  // the workspace is sized for cards of up to 192 SMs
+
+template <int D, int NT, bool SPLIT>
+cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
+    using S = Smem<D, NT, SPLIT>;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
+    if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1u)) {
+        e = cudaFuncSetAttribute(kv4_attention_kernel<D, NT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 S::kBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+    }
+    const int fit = 2 * (S::kBytes + 1024) <= 233472 ? 2 : 1;  // CTAs per SM that shared memory allows
+    const int ctas = std::min(fit * sms, kMaxCtas);
+    kv4_attention_kernel<D, NT, SPLIT><<<ctas, kAttnThreads, S::kBytes, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    kv4_join_kernel<D, NT><<<dim3(ctas, 8 * NT), 128, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D, int NT>
+cudaError_t launch_split(const AttnParams& p, cudaStream_t stream) {
+    return p.dtype == DType::kF32 ? launch_one<D, NT, true>(p, stream) : launch_one<D, NT, false>(p, stream);
+}
+
+template <int D>
+cudaError_t launch_dim(const AttnParams& p, int nt, cudaStream_t stream) {
+    if (nt == 1) return launch_split<D, 1>(p, stream);
+    if (nt == 2) return launch_split<D, 2>(p, stream);
+    if constexpr (D < 256) return launch_split<D, 4>(p, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t kv4_attention_workspace_bytes(int B, int L, int T, int q_heads, int kv_heads, int head_dim) {
+    (void)B;
+    (void)L;
+    const int nt = column_tiles(T, q_heads / kv_heads, head_dim);
+    return static_cast<size_t>(kMaxCtas) * 2 * (8 * nt) * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t stream) {
+    AttnParams p{};
+    p.c = a.c;
+    p.q = a.q;
+    p.out = a.out;
+    p.part = static_cast<float*>(a.workspace);
+    p.q_heads = a.q_heads;
+    p.group = a.q_heads / a.c.kv_heads;
+    p.dtype = a.dtype;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    const int nt = column_tiles(a.c.T, p.group, a.c.head_dim);
+    p.col_blocks = static_cast<int>((static_cast<long long>(a.c.T) * p.group + 8 * nt - 1) / (8 * nt));
+    switch (a.c.head_dim) {
+        case 64: return launch_dim<64>(p, nt, stream);
+        case 128: return launch_dim<128>(p, nt, stream);
+        case 256: return launch_dim<256>(p, nt, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t read_kv4_attention_error(uint32_t* out) {
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv4_attn_error, sizeof(v));
+    if (e != cudaSuccess) return e;
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_kv4_attn_error, &zero, sizeof(zero));
+    *out = v;
+    return e;
+}
+
+}  // namespace gdn

@@ -149,7 +149,12 @@ cudaError_t launch_decode_window_tc(const StepArgs& a, cudaStream_t stream);
 // Reads and clears the tensor-core window kernel's device error word.
 cudaError_t read_window_tc_error(uint32_t* out);
 
-// Synchronises `stream`, then reads and clears the device error words of both kernels.
+// Reads and clears the device error words of the 4-bit cache's and its attention's kernels
+// (gdn_kv4_cache.cu, gdn_kv4_attention.cu).
+cudaError_t read_kv4_cache_error(uint32_t* out);
+cudaError_t read_kv4_attention_error(uint32_t* out);
+
+// Synchronises `stream`, then reads and clears the device error words of all kernels.
 cudaError_t read_device_error(cudaStream_t stream, uint32_t* out);
 
 }  // namespace gdn

@@ -78,7 +78,8 @@ typedef enum gdn_status {
     GDN_ERR_ALIGN = 3,  /* a pointer is not 16-byte aligned (seq_len: 4-byte) */
     GDN_ERR_ALIAS = 4,  /* an output overlaps another buffer of the call */
     GDN_ERR_CUDA = 5,   /* the CUDA runtime refused a query or the launch */
-    GDN_ERR_FLAGS = 6   /* unknown bits in a flags word */
+    GDN_ERR_FLAGS = 6,  /* unknown bits in a flags word */
+    GDN_ERR_DTYPE = 7   /* not a gdn_dtype */
 } gdn_status;
 
 /* Flags of gdn_decode_step_ex. */
@@ -377,6 +378,116 @@ gdn_status gdn_host_pipeline_submit(gdn_host_pipeline* p, const float* qkv, cons
 gdn_status gdn_host_pipeline_synchronize(gdn_host_pipeline* p);
 void gdn_host_pipeline_destroy(gdn_host_pipeline* p);
 
+/*
+ * Operators beside the decode step. A hybrid model's attention layers and the
+ * acceptance of a verify window need these; the conventions are those of the
+ * calls above (device memory, asynchronous on `stream`, capturable in a CUDA
+ * graph, arguments checked on the host, the caller owns all memory), except that
+ * their tensors come in three data types, named by a gdn_dtype.
+ */
+typedef enum gdn_dtype { GDN_DTYPE_F32 = 0, GDN_DTYPE_F16 = 1, GDN_DTYPE_BF16 = 2 } gdn_dtype;
+
+#define GDN_KV4_MAX_T 1048576  /* tokens per sequence in one call of the cache and attention */
+#define GDN_LOGPROBS_MAX_K 32
+
+/*
+ * The 4-bit key/value cache. A block of 16 values along the head dimension is 16
+ * e2m1 codes (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; the sign in bit 3) and one
+ * scale byte b, the fp16 number with the bits b << 7 (5 exponent bits, 3
+ * mantissa bits), 4.5 bits a value:
+ *
+ *   scale = round(min(max |x| / 6, 10240)),  code = round(x / scale)
+ *
+ * each to the nearest value of its grid, ties to even. Values beyond +-61440
+ * saturate and a NaN counts as 0, so a cache holds neither infinities nor NaN. A
+ * cached value has at most 6 significant bits and is exact in fp32, fp16 and bf16.
+ *
+ * The cache is [L][n_pages][page], a page of page_size tokens (a power of two in
+ * [16, 256]) being gdn_kv4_page_bytes() bytes: for each kv head
+ *   [K codes: page_size rows of head_dim/2 bytes][K scales: page_size rows of head_dim/16 bytes]
+ *   [V codes][V scales]
+ * the value 2i of a block in the low nibble of its byte i; block i of row r lies
+ * at block i ^ ((8 (r & 1) + 4 (r >> 2 & 1)) & (head_dim/16 - 1)) of the row.
+ * head_dim is 64, 128 or 256. A fresh cache needs no clearing.
+ *
+ *   block_table [B][max_pages] int32: the pages of sequence b in the order of its
+ *               positions, the same in every layer; entries past a sequence's
+ *               end are never read.
+ *   kv_start    [B] int32: tokens of sequence b in the cache before the window.
+ *   seq_len     [B] int32, or NULL for T: the window's valid tokens, clamped to [0, T].
+ *
+ * The window's token t is at position kv_start[b] + t. A window's tokens that are
+ * not kept need no undoing: the next call's kv_start says where they are overwritten.
+ * A needed entry that is not in [0, n_pages), or a position past max_pages *
+ * page_size, sets bit 1 of the device error word (gdn_read_device_error); that token is not
+ * written, reads as zeros, and takes no part in the attention.
+ */
+size_t gdn_kv4_page_bytes(int kv_heads, int head_dim, int page_size);
+
+/*
+ * gdn_kv4_append - quantises the window's keys and values into the cache.
+ *   k, v [B][L][T][kv_heads][head_dim] (inputs, 16-byte aligned)
+ * Pages of different sequences must differ where they are written.
+ */
+gdn_status gdn_kv4_append(const void* k, const void* v, void* cache, const int32_t* block_table,
+                          const int32_t* kv_start, const int32_t* seq_len, int B, int L, int T, int kv_heads,
+                          int head_dim, int n_pages, int max_pages, int page_size, int dtype, void* stream);
+
+/*
+ * gdn_kv4_read - the cached keys and values of positions kv_start[b] + t.
+ *   k, v [B][L][T][kv_heads][head_dim] (outputs); rows at or past seq_len[b] are not written.
+ * Exact: every cached value fits all three types.
+ */
+gdn_status gdn_kv4_read(const void* cache, const int32_t* block_table, const int32_t* kv_start, const int32_t* seq_len,
+                        void* k, void* v, int B, int L, int T, int kv_heads, int head_dim, int n_pages, int max_pages,
+                        int page_size, int dtype, void* stream);
+
+/*
+ * gdn_kv4_attention - causal attention of the window's queries over the cache, which already holds the
+ * window's own keys and values (gdn_kv4_append). With G = q_heads / kv_heads, for
+ * token t < seq_len[b] and query head h:
+ *
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j),  j = 0 .. kv_start[b] + t,
+ *
+ * over kv head h / G. Rows at or past seq_len[b] are not written; a row that sees no
+ * key (all its pages missing) is zeros.
+ *
+ *   q, out    [B][L][T][q_heads][head_dim] (input, output; 16-byte aligned)
+ *   workspace at least gdn_kv4_attention_workspace_size() bytes, 16-byte aligned,
+ *             owned by the caller; overwritten (partial sums of split sequences)
+ *   scale     positive; usually head_dim^-0.5
+ *
+ * Scores, maxima, sums and the accumulation are fp32. 16-bit queries enter the
+ * products exactly, fp32 ones with 22 bits; probabilities are rounded to 11 bits (22 for fp32 calls).
+ * The result does not depend on timing, but may differ in its last bits between calls of different sizes.
+ */
+size_t gdn_kv4_attention_workspace_size(int B, int L, int T, int q_heads, int kv_heads, int head_dim);
+gdn_status gdn_kv4_attention(const void* q, const void* cache, const int32_t* block_table, const int32_t* kv_start,
+                             const int32_t* seq_len, void* out, void* workspace, size_t workspace_bytes, int B, int L,
+                             int T, int q_heads, int kv_heads, int head_dim, int n_pages, int max_pages, int page_size,
+                             int dtype, float scale, void* stream);
+
+/*
+ * gdn_logprobs - log probabilities of given tokens, entropy and the k most likely
+ * tokens of rows of logits, in one pass over them:
+ *
+ *   logprob[i] = x[i][tokens[i]] - lse_i,  lse_i = log sum_j exp(x[i][j])
+ *   entropy[i] = - sum_j p_j log p_j
+ *   top_ids[i][0..k), top_logprobs[i][0..k): by falling value, equal values by rising index
+ *
+ *   logits [n_rows][row_stride >= vocab] of a gdn_dtype (input, aligned to its elements)
+ *   tokens [n_rows] int32 (input; NULL if logprob is); an id outside [0, vocab) gives a NaN logprob
+ *   logprob, entropy [n_rows] fp32 (outputs, either may be NULL)
+ *   top_ids int32, top_logprobs fp32 [n_rows][k] (outputs, ignored for k = 0); k <= min(vocab, GDN_LOGPROBS_MAX_K)
+ *
+ * Logits of -inf have probability 0. A row whose largest logit is not finite (all
+ * -inf, a +inf, a NaN) has no distribution: its values are NaN, and its
+ * top_ids go by the order of the logits, NaN first. Needs no workspace.
+ */
+gdn_status gdn_logprobs(const void* logits, const int32_t* tokens, float* logprob, float* entropy, int32_t* top_ids,
+                        float* top_logprobs, int64_t n_rows, int64_t vocab, int64_t row_stride, int k, int dtype,
+                        void* stream);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* gdn_last_error(void);
 
@@ -399,8 +510,9 @@ gdn_status gdn_get_geometry(int32_t out[8]);
 /*
  * Reads and clears the kernel's device error word on the current device,
  * after synchronising `stream`. 0 means no kernel reported an error; bit 0
- * means a wait for a state tile gave up after its time limit (the kernel then
- * stopped early and its outputs are not valid).
+ * means a wait for a state tile (or a cache tile) gave up after its time limit (the kernel then
+ * stopped early and its outputs are not valid); bit 1 means a page that a gdn_kv4
+ * call needed was missing from its block_table.
  */
 gdn_status gdn_read_device_error(void* stream, uint32_t* out);
 
