@@ -113,6 +113,10 @@ def _check(status: int):
 
 
 def _ptr(t, name, shape, dtype=torch.float32, device=None, optional=False):
+    # the usual case first: a call's checks are most of its cost on the host
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()
+            and (device is None or t.device == device)):
+        return t.data_ptr()
     if t is None:
         if optional:
             return None
@@ -419,6 +423,24 @@ def gdn_step_inputs_packed(x, packed, dt, ssm_a, qkv, z, gate, beta, workspace, 
                                           int(workspace.numel()), B, L, T, E, _stream_handle(stream, dev)))
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _run(fn, dev, stream, *args):
+    """Calls a C entry point (its last argument the stream) with ``dev`` as the current device."""
+    if stream is None and _raw_stream is not None:
+        handle = _raw_stream(dev.index)
+    else:
+        handle = _stream_handle(stream, dev)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != 0:
+        _check(status)
+
+
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
@@ -435,14 +457,12 @@ def gdn_kv4_page_bytes(kv_heads: int, head_dim: int, page_size: int) -> int:
 
 def _kv4(cache, block_table, kv_start, seq_len, B, L, kv_heads, head_dim, page_size, dev):
     """Checked pointers (cache, block_table, kv_start, seq_len), n_pages and max_pages of a cache call."""
-    page_bytes = gdn_kv4_page_bytes(kv_heads, head_dim, page_size)
-    if page_bytes == 0:
-        raise GdnError(2, f"kv_heads={kv_heads}, head_dim={head_dim}, page_size={page_size} are not a cache's sizes")
     if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
         raise ValueError("cache must be a [L][n_pages][page_bytes] tensor")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a [B][max_pages] tensor")
-    n_pages, max_pages = int(cache.shape[1]), int(block_table.shape[1])
+    page_bytes = 2 * kv_heads * page_size * (head_dim // 2 + head_dim // 16)  # the library checks the three
+    n_pages, max_pages = cache.shape[1], block_table.shape[1]
     return (
         _ptr(cache, "cache", (L, n_pages, page_bytes), dtype=torch.uint8, device=dev),
         _ptr(block_table, "block_table", (B, max_pages), dtype=torch.int32, device=dev),
@@ -465,12 +485,10 @@ def gdn_kv4_append(k, v, cache, block_table, kv_start, page_size, seq_len=None, 
     [B][max_pages]; ``kv_start`` and the optional ``seq_len`` (valid tokens) are int32 [B]."""
     lib = load_library()
     dt, kp, vp = _kv_shape(k, v)
-    B, L, T, H, D = (int(n) for n in k.shape)
+    B, L, T, H, D = k.shape
     dev = k.device
     (cp, bt, ks, sl), n_pages, max_pages = _kv4(cache, block_table, kv_start, seq_len, B, L, H, D, page_size, dev)
-    with torch.cuda.device(dev):
-        _check(lib.gdn_kv4_append(kp, vp, cp, bt, ks, sl, B, L, T, H, D, n_pages, max_pages, int(page_size), dt,
-                                  _stream_handle(stream, dev)))
+    _run(lib.gdn_kv4_append, dev, stream, kp, vp, cp, bt, ks, sl, B, L, T, H, D, n_pages, max_pages, page_size, dt)
 
 
 def gdn_kv4_read(cache, block_table, kv_start, k, v, page_size, seq_len=None, stream=None):
@@ -478,12 +496,10 @@ def gdn_kv4_read(cache, block_table, kv_start, k, v, page_size, seq_len=None, st
     [B][L][T][kv_heads][head_dim]); rows at or past ``seq_len[b]`` are not written."""
     lib = load_library()
     dt, kp, vp = _kv_shape(k, v)
-    B, L, T, H, D = (int(n) for n in k.shape)
+    B, L, T, H, D = k.shape
     dev = k.device
     (cp, bt, ks, sl), n_pages, max_pages = _kv4(cache, block_table, kv_start, seq_len, B, L, H, D, page_size, dev)
-    with torch.cuda.device(dev):
-        _check(lib.gdn_kv4_read(cp, bt, ks, sl, kp, vp, B, L, T, H, D, n_pages, max_pages, int(page_size), dt,
-                                _stream_handle(stream, dev)))
+    _run(lib.gdn_kv4_read, dev, stream, cp, bt, ks, sl, kp, vp, B, L, T, H, D, n_pages, max_pages, page_size, dt)
 
 
 def gdn_kv4_attention_workspace_size(B: int, L: int, T: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -502,19 +518,16 @@ def gdn_kv4_attention(q, cache, block_table, kv_start, out, workspace, page_size
     if not isinstance(q, torch.Tensor) or q.dim() != 5:
         raise ValueError("q must be a [B][L][T][q_heads][head_dim] tensor")
     dt = _dtype(q, "q")
-    B, L, T, H, D = (int(n) for n in q.shape)
+    B, L, T, H, D = q.shape
     dev = q.device
     if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or workspace.dim() != 1:
         raise TypeError("workspace must be a 1-D torch.uint8 tensor")
     qp = _ptr(q, "q", q.shape, dtype=q.dtype)
     op = _ptr(out, "out", q.shape, dtype=q.dtype, device=dev)
     wp = _ptr(workspace, "workspace", tuple(workspace.shape), dtype=torch.uint8, device=dev)
-    (cp, bt, ks, sl), n_pages, max_pages = _kv4(cache, block_table, kv_start, seq_len, B, L, int(kv_heads), D, page_size,
-                                                dev)
-    with torch.cuda.device(dev):
-        _check(lib.gdn_kv4_attention(qp, cp, bt, ks, sl, op, wp, int(workspace.numel()), B, L, T, H, int(kv_heads), D,
-                                     n_pages, max_pages, int(page_size), dt, D ** -0.5 if scale is None else float(scale),
-                                     _stream_handle(stream, dev)))
+    (cp, bt, ks, sl), n_pages, max_pages = _kv4(cache, block_table, kv_start, seq_len, B, L, kv_heads, D, page_size, dev)
+    _run(lib.gdn_kv4_attention, dev, stream, qp, cp, bt, ks, sl, op, wp, workspace.numel(), B, L, T, H, kv_heads, D,
+         n_pages, max_pages, page_size, dt, D ** -0.5 if scale is None else scale)
 
 
 def gdn_logprobs(logits, tokens=None, logprob=None, entropy=None, top_ids=None, top_logprobs=None, stream=None):
@@ -528,8 +541,8 @@ def gdn_logprobs(logits, tokens=None, logprob=None, entropy=None, top_ids=None, 
         raise ValueError("logits must be a [N][vocab] tensor")
     if logits.device.type != "cuda":
         raise ValueError(f"logits must be a CUDA tensor, got one on {logits.device}")
-    N, V = (int(n) for n in logits.shape)
-    ld = int(logits.stride(0)) if N > 1 else V
+    N, V = logits.shape
+    ld = logits.stride(0) if N > 1 else V
     if (V > 1 and logits.stride(1) != 1) or ld < V:
         raise ValueError("each row of logits must be contiguous, and rows may not overlap")
     if (logprob is None) != (tokens is None):
@@ -541,7 +554,7 @@ def gdn_logprobs(logits, tokens=None, logprob=None, entropy=None, top_ids=None, 
     if top_ids is not None:
         if not isinstance(top_ids, torch.Tensor) or top_ids.dim() != 2:
             raise ValueError("top_ids must be a [N][k] tensor")
-        k = int(top_ids.shape[1])
+        k = top_ids.shape[1]
     p = [
         _ptr(tokens, "tokens", (N,), dtype=torch.int32, device=dev, optional=True),
         _ptr(logprob, "logprob", (N,), device=dev, optional=True),
@@ -549,8 +562,7 @@ def gdn_logprobs(logits, tokens=None, logprob=None, entropy=None, top_ids=None, 
         _ptr(top_ids, "top_ids", (N, k), dtype=torch.int32, device=dev, optional=True),
         _ptr(top_logprobs, "top_logprobs", (N, k), device=dev, optional=True),
     ]
-    with torch.cuda.device(dev):
-        _check(lib.gdn_logprobs(logits.data_ptr(), *p, N, V, ld, k, dt, _stream_handle(stream, dev)))
+    _run(lib.gdn_logprobs, dev, stream, logits.data_ptr(), *p, N, V, ld, k, dt)
 
 
 DISPATCH_KERNELS = {1: "gdn_decode_t1_kernel", 2: "gdn_window_kernel", 3: "gdn_chunk_kernel", 4: "gdn_window_tc_kernel"}

@@ -28,7 +28,7 @@
 // Numerics. Queries are scaled by a power of two per row to fill fp16's range
 // (16-bit inputs stay exact; fp32 ones are split into fp16 hi + lo, 22 bits);
 // scores, maxima, sums and outputs are fp32. Probabilities are rounded to fp16
-// (half a step is 2^-12 of the value, below the 2^-9 of a bf16 output; 2^14 is the largest, so that small ones
+// (half a step is 2^-12 of the value, below the 2^-9 of a bf16 output; the reference maximum stands for 2^8, so that small ones
 // keep their bits) or, for fp32, split into hi + lo. Masked keys take no part: their
 // scores are set to -inf by a select, and the scales of tokens past the end
 // are set to zero, so whatever such bytes hold (infinities, NaN) does not matter.
@@ -40,8 +40,9 @@
 // second small kernel joins them in order: no atomics, so results do not
 // depend on timing.
 //
-// Waits are bounded; one that gives up stops that warp's work, sets the device error word and
-// drains the copies in flight before the CTA returns.
+// Each warp fills its own ring of tiles by 16-byte asynchronous copies: bulk copies take uniform
+// operands, and the four small pieces of a tile cost more instructions that way (27 per
+// mma, against 20). No warp waits for another but at the joins, and nothing spins.
 
 #include <algorithm>
 #include <atomic>
@@ -55,19 +56,21 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kAttnThreads = 32 * kWarps;
-constexpr int kStages = 4;
-constexpr uint32_t kCodeBytes = 2048;   // a tile's K (or V) codes: 4096 / D tokens
-constexpr uint32_t kScaleBytes = 256;   // and their scales
-constexpr uint32_t kStageBytes = 2 * (kCodeBytes + kScaleBytes);
-constexpr float kPShift = 14.0f;        // the largest probability is 2^14
+constexpr float kPShift = 8.0f;  // probabilities are kept relative to 2^-8 of the reference maximum ...
+constexpr float kSlack = 6.0f;   // ... which is raised when a score exceeds it by 6: none is above 2^14
+constexpr float kNone = 1e30f;   // the shift of a column that has seen no key
 
 __device__ unsigned int g_kv4_attn_error = 0;
 
+// A warp's tile: kTokens tokens of one kv head, K codes | V codes | K scales | V scales.
 template <int D>
 struct Tile {
-    static constexpr int kTokens = 4096 / D;
+    static constexpr int kTokens = D == 64 ? 64 : 32;
     static constexpr int kRow = D / 2;      // code bytes of a token
     static constexpr int kBlocks = D / 16;  // scales of a token
+    static constexpr uint32_t kCodeBytes = kTokens * kRow;
+    static constexpr uint32_t kScaleBytes = kTokens * kBlocks;
+    static constexpr uint32_t kBytes = 2 * (kCodeBytes + kScaleBytes);
 };
 
 struct AttnParams {
@@ -99,10 +102,15 @@ struct Cursor {
     long long left;  // rounds still to do in this CTA, this one included
 };
 
-// Rounds [lo, hi) of CTA i of n.
+// Rounds [lo, hi) of CTA i of n <= total: each has one at least.
 __device__ __forceinline__ void cta_range(long long total, int i, int n, long long& lo, long long& hi) {
     lo = total * i / n;
     hi = total * (i + 1) / n;
+}
+
+// The CTA of n that has round x: the largest i with total i / n <= x.
+__device__ __forceinline__ int cta_of(long long total, long long x, int n) {
+    return static_cast<int>(((x + 1) * n - 1) / total);
 }
 
 // Sum of the sequences' rounds, by one warp.
@@ -178,6 +186,12 @@ __device__ __forceinline__ Unit unit_of(const AttnParams& p, int b, int u, int c
 }
 
 // ---------------------------------------------------------------- pieces --
+// Waits until at most N of this thread's committed cp.async groups are still in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile(
@@ -206,10 +220,12 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t s, uint32_t (&v)[4])
     for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(s));
 }
 
-// Scale byte i (0 or 1) of a 16-bit pair of them, as both halves of an fp16 pair.
-__device__ __forceinline__ uint32_t scale_pair(uint32_t two, int i) {
-    const uint32_t s = ((two >> (8 * i)) & 255u) << 7;
-    return s | (s << 16);
+// Byte i (0 or 1) of a as both halves of an fp16 pair of scales, and byte i of a and of b as its halves.
+__device__ __forceinline__ uint32_t scale_twice(uint32_t a, int i) { return __byte_perm(a, 0, i ? 0x4141 : 0x4040) << 7; }
+template <int D>
+__device__ __forceinline__ uint32_t scale_both(uint32_t a, uint32_t b, int i) {
+    if constexpr (D < 256) return __byte_perm(a, b, 0x5410) << 7;  // a and b have one byte each
+    return (__byte_perm(a, b, i ? 0x5511 : 0x4400) & 0x00FF00FFu) << 7;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -266,100 +282,168 @@ __device__ __forceinline__ int dim_of(int pos) {
 }
 
 // ---------------------------------------------------------------- kernel --
+// Resident CTAs per SM (a block's registers and shared memory allow them) and tiles in a warp's ring.
 template <int D, int NT, bool SPLIT>
-struct Smem {
-    static constexpr int kCols = 8 * NT;
-    static constexpr uint32_t kRedStride = D + 8;  // floats: bank spread of the lanes' pairs
-    static constexpr uint32_t kQBytes = kCols * D * 2 * (SPLIT ? 2 : 1);
-    static constexpr uint32_t kOffQ = kWarps * kStages * kStageBytes;
-    static constexpr uint32_t kOffRed = kOffQ + kQBytes;
-    static constexpr uint32_t kOffCol = kOffRed + kWarps * 8 * kRedStride * 4;  // maxima and sums: [warp][col] twice
-    static constexpr uint32_t kOffMul = kOffCol + 2 * kWarps * kCols * 4;     // per column: scale of the raw scores
-    static constexpr uint32_t kOffBad = kOffMul + kCols * 4;                  // per stage: pages that are not there
-    static constexpr uint32_t kOffBar = kOffBad + kWarps * kStages * 4;
-    static constexpr uint32_t kBytes = kOffBar + kWarps * kStages * 8;
+struct Shape {
+    static constexpr int kCtas = D == 256 ? 2 : NT == 1 ? 3 : 2;
+    static constexpr int kStages = D == 256 ? 2 : NT == 1 ? 3 : 4;
 };
 
 template <int D, int NT, bool SPLIT>
-__global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __grid_constant__ AttnParams p) {
+struct Smem {
+    static constexpr int kStages = Shape<D, NT, SPLIT>::kStages;
+    static constexpr int kCols = 8 * NT;
+    static constexpr uint32_t kRedStride = D + 8;  // floats: bank spread of the lanes' pairs
+    static constexpr uint32_t kQBytes = kCols * D * 2 * (SPLIT ? 2 : 1);
+    static constexpr uint32_t kOffQ = kWarps * kStages * Tile<D>::kBytes;
+    static constexpr uint32_t kOffCol = kOffQ + kQBytes;                   // maxima and sums: [warp][col] twice
+    static constexpr uint32_t kOffMul = kOffCol + 2 * kWarps * kCols * 4;  // per column: scale of the raw scores
+    static constexpr uint32_t kOffBad = kOffMul + kCols * 4;               // per stage: pages that are not there
+    static constexpr uint32_t kOffRed = kOffBad + kWarps * kStages * 4;    // per warp: its stage with its sums, or -1
+    static constexpr uint32_t kBytes = kOffRed + kWarps * 4;
+    static_assert(8 * kRedStride * 4 <= Tile<D>::kBytes, "eight columns of sums fit a stage");
+};
+
+template <int D, int NT, bool SPLIT>
+__global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
+    kv4_attention_kernel(const __grid_constant__ AttnParams p) {
     using S = Smem<D, NT, SPLIT>;
     using TL = Tile<D>;
+    constexpr int kStages = S::kStages;
     constexpr int kCols = S::kCols;
     constexpr int kTokens = TL::kTokens, kHalfTiles = kTokens / 16;  // m16 tiles of a tile
+    constexpr int kRound = kTokens * kWarps;
     constexpr int kMTiles = D / 16;
+    constexpr bool kQRegs = NT == 1 && !SPLIT && D <= 128;  // the query fragments stay in registers
     extern __shared__ __align__(128) unsigned char sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-    float* red = reinterpret_cast<float*>(sm + S::kOffRed);
     float* col_m = reinterpret_cast<float*>(sm + S::kOffCol);
     float* col_l = col_m + kWarps * kCols;
     float* mul_s = reinterpret_cast<float*>(sm + S::kOffMul);
     uint32_t* bad_s = reinterpret_cast<uint32_t*>(sm + S::kOffBad) + warp * kStages;
-    const uint32_t bars = smem_addr(sm + S::kOffBar) + warp * kStages * 8;
-    unsigned char* ring = sm + warp * kStages * kStageBytes;
-    const uint32_t ring_addr = smem_addr(ring);
-    if (lane == 0) {
-        for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
-        fence_mbar_init();
-    }
-    __syncwarp();
-
+    int* red_s = reinterpret_cast<int*>(sm + S::kOffRed);
+    unsigned char* ring = sm + warp * kStages * TL::kBytes;
     const int units = p.c.L * p.c.kv_heads * p.col_blocks;
     const long long total = all_rounds<D>(p.c, lane) * units;
+    const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+    if (static_cast<int>(blockIdx.x) >= ctas) return;
     long long lo, hi;
-    cta_range(total, blockIdx.x, gridDim.x, lo, hi);
-    if (lo == hi) return;
+    cta_range(total, blockIdx.x, ctas, lo, hi);
     Cursor cur = locate<D>(p.c, units, lo, lane);
     cur.left = hi - lo;
 
+    // --- requests: 16 bytes per lane and copy, 512 of codes at a time; lane j looks up page j of the tile
     const int psize = 1 << p.c.page_shift;
-    const int piece_rows = min(psize, kTokens);
     const int piece_shift = min(p.c.page_shift, 31 - __clz(kTokens));
-    const int n_pieces = 4 * (kTokens / piece_rows);
-    bool failed = false;
-    uint32_t issued = 0, used = 0;  // this warp's tiles
-    Cursor ahead = cur;
-    Unit au = unit_of(p, ahead.b, ahead.u, kCols);
-
-    // Requests the next tile of this warp (skipping rounds in which it has none).
-    auto issue = [&]() {
-        while (ahead.left > 0) {
-            const int p0 = (ahead.r * kWarps + warp) * kTokens;
-            const bool have = p0 < au.end;
-            const int b = ahead.b, l = au.l, h = au.h, end = au.end;
-            const int old_b = ahead.b, old_u = ahead.u;
-            advance<D>(p.c, units, ahead);
-            if (ahead.left > 0 && (ahead.b != old_b || ahead.u != old_u)) au = unit_of(p, ahead.b, ahead.u, kCols);
-            if (!have) continue;
-            const uint32_t s = issued % kStages;
-            const int j = lane >> 2, kind = lane & 3;  // piece: page j of the tile; K codes, K scales, V codes, V scales
-            const int pos = p0 + j * piece_rows;
-            const bool want = lane < n_pieces && pos < end;
-            const int page = want ? kv4_page(p.c, b, pos) : -1;
-            const bool ok = page >= 0;
-            const unsigned there = __ballot_sync(~0u, ok);
-            const unsigned wanted = __ballot_sync(~0u, want);
-            if (lane == 0) {
-                bad_s[s] = there ^ wanted;
-                mbar_arrive_expect_tx(bars + 8 * s, __popc(there) / 4 * 2 * piece_rows * (TL::kRow + TL::kBlocks));
+    const int n_pages = kTokens >> piece_shift;  // of a tile
+    const uint32_t head_bytes = static_cast<uint32_t>(kv4_head_bytes(psize, D)), page_bytes = head_bytes * p.c.kv_heads;
+    // a lane's place in the first copy of the scales: of K in the lower half (D < 256: K and V in one copy)
+    const uint32_t scale_lane = TL::kScaleBytes == 256 ? (lane & 15) * 16 + (lane >> 4) * (head_bytes / 2) : lane * 16;
+    const uint32_t ring_addr = smem_addr(ring) + lane * 16;
+    Cursor ahead = cur;     // unit of the next tile
+    int a_seg = 0;          // rounds of that unit left in this CTA
+    int a_p0 = 0, a_end = 0;
+    int a_page = -1;        // block table entry of the tile's page; of page `lane` if it has several
+    const int32_t* a_table = nullptr;
+    const uint8_t* a_head = nullptr;
+    bool ready = false;     // there is a next tile
+    // The warp's next tile: its page's number is read here, a tile ahead of its use.
+    auto look = [&]() {
+        while (a_p0 >= a_end || a_seg <= 0) {  // on to the next unit in which the warp has a tile
+            if (ahead.left <= 0) {
+                ready = false;
+                return;
             }
-            __syncwarp();
-            if (ok) {
-                const int row = pos & (psize - 1);
-                const uint8_t* src = p.c.cache + kv4_head_offset(p.c, l, page, h) +
-                                     ((kind & 2) ? kv4_head_bytes(psize, D) / 2 : 0);
-                uint32_t dst = ring_addr + s * kStageBytes;
-                if (kind & 1)
-                    bulk_load(dst + 2 * kCodeBytes + (kind >> 1) * kScaleBytes + j * piece_rows * TL::kBlocks,
-                              src + psize * TL::kRow + row * TL::kBlocks, piece_rows * TL::kBlocks, bars + 8 * s);
-                else
-                    bulk_load(dst + (kind >> 1) * kCodeBytes + j * piece_rows * TL::kRow, src + row * TL::kRow,
-                              piece_rows * TL::kRow, bars + 8 * s);
+            const Unit u = unit_of(p, ahead.b, ahead.u, kCols);
+            a_end = u.end;
+            a_head = p.c.cache + (static_cast<size_t>(u.l) * p.c.n_pages * p.c.kv_heads + u.h) * head_bytes;
+            a_table = p.c.block_table + static_cast<size_t>(ahead.b) * p.c.max_pages;
+            a_seg = static_cast<int>(min(static_cast<long long>(ahead.rounds - ahead.r), ahead.left));
+            a_p0 = ahead.r * kRound + warp * kTokens;
+            ahead.r += a_seg - 1;
+            ahead.left -= a_seg - 1;
+            advance<D>(p.c, units, ahead);
+        }
+        ready = true;
+        const int slot = (a_p0 >> p.c.page_shift) + (n_pages == 1 ? 0 : lane);
+        a_page = n_pages == 1 || (lane < n_pages && a_p0 + (lane << piece_shift) < a_end) ? __ldg(a_table + slot) : 0;
+    };
+    uint32_t issued = 0, used = 0;  // this warp's tiles
+    auto issue = [&]() {
+        if (ready) {
+            const uint32_t s = issued % kStages;
+            const bool gone = static_cast<uint32_t>(a_page) >= static_cast<uint32_t>(p.c.n_pages);
+            const int a_row = a_p0 & (psize - 1);
+            const unsigned bad = n_pages == 1 ? (gone ? 1u : 0u) : __ballot_sync(~0u, gone);
+            if (lane == 0) bad_s[s] = bad;
+            if (gone) a_page = -1;
+            const uint32_t dst = ring_addr + s * TL::kBytes;
+            const uint32_t half = static_cast<uint32_t>(head_bytes / 2), scales = psize * TL::kRow;
+            constexpr int kCopies = TL::kCodeBytes / 512, kRows = 512 / TL::kRow;  // of K or V codes; rows of a copy
+            constexpr int kScaleCopies = 2 * TL::kScaleBytes / 512;                // K's, then V's
+            if (n_pages == 1) {
+                if (!gone) {
+                    const uint8_t* src = a_head + static_cast<unsigned long long>(static_cast<uint32_t>(a_page)) * page_bytes;
+                    const uint8_t* k = src + a_row * TL::kRow + lane * 16;
+                    const uint8_t* v = k + half;
+#pragma unroll
+                    for (int i = 0; i < kCopies; ++i) {
+                        cp_async16(dst + i * 512, k + i * 512);
+                        cp_async16(dst + TL::kCodeBytes + i * 512, v + i * 512);
+                    }
+                    const uint8_t* c = src + scales + a_row * TL::kBlocks + scale_lane;
+#pragma unroll
+                    for (int i = 0; i < kScaleCopies; ++i)
+                        cp_async16(dst + 2 * TL::kCodeBytes + i * 512, kScaleCopies == 1 ? c : c + i * half);
+                }
+            } else {  // pages end between copies
+#pragma unroll 1
+                for (int i = 0; i < kCopies; ++i) {
+                    const int j = (i * kRows) >> piece_shift;
+                    const int page = __shfl_sync(~0u, a_page, j);
+                    const uint8_t* k = a_head + static_cast<unsigned long long>(static_cast<uint32_t>(page)) * page_bytes +
+                                       (i * kRows - (j << piece_shift)) * TL::kRow + lane * 16;
+                    if (page >= 0) {
+                        cp_async16(dst + i * 512, k);
+                        cp_async16(dst + TL::kCodeBytes + i * 512, k + half);
+                    }
+                }
+#pragma unroll 1
+                for (int i = 0; i < kScaleCopies; ++i) {
+                    const int at = (i * 512 + lane * 16) & (TL::kScaleBytes - 1), part = (i * 512 + lane * 16) / TL::kScaleBytes;
+                    const int row = at / TL::kBlocks, j = row >> piece_shift;
+                    const int page = __shfl_sync(~0u, a_page, j);
+                    if (page >= 0)
+                        cp_async16(dst + 2 * TL::kCodeBytes + i * 512,
+                                   a_head + static_cast<unsigned long long>(static_cast<uint32_t>(page)) * page_bytes +
+                                       part * half + scales + (row - (j << piece_shift)) * TL::kBlocks + (at & (TL::kBlocks - 1)));
+                }
             }
             ++issued;
-            return;
+            a_p0 += kRound;
+            --a_seg;
+            look();
         }
+        cp_async_commit();  // one group per place in the ring, empty or not
     };
+    look();
     for (int s = 0; s < kStages; ++s) issue();
+    griddep_launch_dependents();  // the join's CTAs may come up; they wait for this grid's end
+
+    // --- where this lane reads a tile (rows 8 and 16 further have the same swizzle)
+    const int ka = pi8(g), v0 = pi8(2 * t4), v1 = pi8(2 * t4 + 1);
+    const uint32_t k_off = ka * TL::kRow + (D >= 128 ? ((2 * t4) ^ kv4_swizzle(ka, TL::kBlocks)) * 8 : t4 * 8);
+    const uint32_t k_off2 = ka * TL::kRow + ((8 + 2 * t4) ^ kv4_swizzle(ka, TL::kBlocks)) * 8;  // D = 256: its second half
+    const uint32_t ks_off = 2 * TL::kCodeBytes + ka * TL::kBlocks + (D >= 128 ? 2 * t4 : t4);
+    auto v_at = [&](int row) -> uint32_t {
+        if constexpr (D == 256) return row * TL::kRow + ((2 * g) ^ kv4_swizzle(row, TL::kBlocks)) * 8;
+        if constexpr (D == 128) return row * TL::kRow + (g ^ kv4_swizzle(row, TL::kBlocks)) * 8;
+        return row * TL::kRow + g * 4;
+    };
+    const uint32_t v_off0 = TL::kCodeBytes + v_at(v0), v_off1 = TL::kCodeBytes + v_at(v1);
+    const int vs_lane = D == 256 ? 2 * g : D == 128 ? g : g >> 1;
+    const uint32_t vs_off0 = 2 * TL::kCodeBytes + TL::kScaleBytes + v0 * TL::kBlocks + vs_lane;
+    const uint32_t vs_off1 = 2 * TL::kCodeBytes + TL::kScaleBytes + v1 * TL::kBlocks + vs_lane;
 
     while (cur.left > 0) {
         const Unit x = unit_of(p, cur.b, cur.u, kCols);
@@ -386,7 +470,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __
             // f = 2^(11 - exponent of the largest magnitude): the row fills fp16's range, exactly
             const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -115), 127);
             const float f = a > 0.0f && a <= 3.0e38f ? __uint_as_float(static_cast<uint32_t>(138 - e) << 23) : 1.0f;
-            if (lane == 0) mul_s[c] = p.scale_log2 / f;
+            if (lane == 0) mul_s[c] = fmaxf(p.scale_log2 / f, 1.17549435e-38f);  // never 0: 0 times a masked -inf
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 if (4 * lane + 128 * i >= D) continue;
@@ -402,8 +486,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __
             }
         }
         __syncthreads();
+        uint2 qr[kQRegs ? D / 16 : 1];
+        if constexpr (kQRegs) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) qr[i] = *reinterpret_cast<const uint2*>(sm + S::kOffQ + (i * 32 + lane) * 8);
+        }
 
-        float m[NT][2], ls[NT][2], mul[NT][2];
+        float m[NT][2], shift[NT][2], ls[NT][2], mul[NT][2];
         int lim[NT][2];  // last position that the column sees
         float o[kMTiles][NT][4];
 #pragma unroll
@@ -412,6 +501,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __
             for (int j = 0; j < 2; ++j) {
                 const int c = 8 * nt + 2 * t4 + j;
                 m[nt][j] = -INFINITY;
+                shift[nt][j] = kNone;
                 ls[nt][j] = 0.0f;
                 mul[nt][j] = mul_s[c];
                 lim[nt][j] = c < all_cols ? min(x.start + (x.col0 + c) / p.group, x.end - 1) : -1;
@@ -422,18 +512,20 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
-        // positions below this are seen by every column of the block
-        const int seen_by_all = all_cols == kCols ? min(x.start + x.col0 / p.group + 1, x.end) : 0;
+        // positions below this are seen by every column that exists (the others' results are not used)
+        const int seen_by_all = min(x.start + x.col0 / p.group + 1, x.end);
+        bool owed = false;  // a consumed stage is not yet refilled
+        int freed = -1;     // the last consumed stage
 
         for (int r = r0; r < r1; ++r) {
-            const int p0 = (r * kWarps + warp) * kTokens;
-            if (p0 >= x.end || failed) continue;
+            const int p0 = r * kRound + warp * kTokens;
+            if (p0 >= x.end) break;
+            if (owed) issue();
+            owed = false;
             const uint32_t s = used % kStages;
-            if (!mbar_wait_bounded(bars + 8 * s, (used / kStages) & 1u)) {
-                failed = true;
-                continue;
-            }
-            const unsigned char* st = ring + s * kStageBytes;
+            cp_async_wait<kStages - 1>();
+            __syncwarp();  // every lane's copies of the stage have landed
+            const unsigned char* st = ring + s * TL::kBytes;
             const uint32_t bad = bad_s[s];
             const bool whole = p0 + kTokens <= seen_by_all && bad == 0;
 
@@ -441,11 +533,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __
             float sc[kHalfTiles][NT][4];
 #pragma unroll
             for (int mt = 0; mt < kHalfTiles; ++mt) {
-                const int ra = 16 * mt + pi8(g), rb = ra + 8;
-                const uint8_t* ka = st + ra * TL::kRow;
-                const uint8_t* kb = st + rb * TL::kRow;
-                const uint8_t* sa = st + 2 * kCodeBytes + ra * TL::kBlocks;
-                const uint8_t* sb = st + 2 * kCodeBytes + rb * TL::kBlocks;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -456,34 +543,39 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __
                     constexpr int kWords = D >= 128 ? 4 : 2;
                     uint32_t wa[kWords], wb[kWords];
                     uint32_t da, db;  // scale bytes of the lane's blocks
+                    const unsigned char* kp = st + (hf == 0 ? k_off : k_off2) + mt * 16 * TL::kRow;
+                    const unsigned char* sp = st + ks_off + 8 * hf + mt * 16 * TL::kBlocks;
                     if constexpr (D >= 128) {
-                        const int blk = 8 * hf + 2 * t4;
-                        const uint4 va = *reinterpret_cast<const uint4*>(ka + (blk ^ kv4_swizzle(ra, TL::kBlocks)) * 8);
-                        const uint4 vb = *reinterpret_cast<const uint4*>(kb + (blk ^ kv4_swizzle(rb, TL::kBlocks)) * 8);
+                        const uint4 va = *reinterpret_cast<const uint4*>(kp);
+                        const uint4 vb = *reinterpret_cast<const uint4*>(kp + 8 * TL::kRow);
                         wa[0] = va.x, wa[1] = va.y, wa[2] = va.z, wa[3] = va.w;
                         wb[0] = vb.x, wb[1] = vb.y, wb[2] = vb.z, wb[3] = vb.w;
-                        da = *reinterpret_cast<const uint16_t*>(sa + blk);
-                        db = *reinterpret_cast<const uint16_t*>(sb + blk);
+                        da = *reinterpret_cast<const uint16_t*>(sp);
+                        db = *reinterpret_cast<const uint16_t*>(sp + 8 * TL::kBlocks);
                     } else {
-                        const uint2 va = *reinterpret_cast<const uint2*>(ka + t4 * 8);
-                        const uint2 vb = *reinterpret_cast<const uint2*>(kb + t4 * 8);
+                        const uint2 va = *reinterpret_cast<const uint2*>(kp);
+                        const uint2 vb = *reinterpret_cast<const uint2*>(kp + 8 * TL::kRow);
                         wa[0] = va.x, wa[1] = va.y;
                         wb[0] = vb.x, wb[1] = vb.y;
-                        da = sa[t4];
-                        db = sb[t4];
+                        da = sp[0];
+                        db = sp[8 * TL::kBlocks];
                     }
 #pragma unroll
                     for (int w = 0; w < kWords; ++w) {
                         uint32_t a[4], c[4];
-                        unpack(wa[w], scale_pair(da, w >> 1), a);
-                        unpack(wb[w], scale_pair(db, w >> 1), c);
+                        unpack(wa[w], scale_twice(da, w >> 1), a);
+                        unpack(wb[w], scale_twice(db, w >> 1), c);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const int step = 8 * hf + 2 * w + k;
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 const uint32_t at = ((step * NT + nt) * 32 + lane) * 8;
-                                const uint2 qh = *reinterpret_cast<const uint2*>(sm + S::kOffQ + at);
+                                uint2 qh;
+                                if constexpr (kQRegs)
+                                    qh = qr[step];
+                                else
+                                    qh = *reinterpret_cast<const uint2*>(sm + S::kOffQ + at);
                                 mma_f16(sc[mt][nt], a[2 * k], c[2 * k], a[2 * k + 1], c[2 * k + 1], qh.x, qh.y);
                                 if constexpr (SPLIT) {
                                     const uint2 ql = *reinterpret_cast<const uint2*>(sm + S::kOffQ + kCols * D * 2 + at);
@@ -495,43 +587,46 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __
                 }
             }
 
-            // --- running maximum, probabilities
-            float nm[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                nm[nt][0] = m[nt][0];
-                nm[nt][1] = m[nt][1];
+            // --- masks; the reference maximum is raised when a score is well above it
+            if (!whole) {
 #pragma unroll
                 for (int mt = 0; mt < kHalfTiles; ++mt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float v = sc[mt][nt][j] * mul[nt][j & 1];
-                        if (!whole) {
-                            const int row = 16 * mt + pi8(g) + 8 * (j >> 1);
-                            const bool gone = (bad >> (4 * (row >> piece_shift))) & 1u;
-                            if (p0 + row > lim[nt][j & 1] || gone) v = -INFINITY;
-                        }
-                        sc[mt][nt][j] = v;
-                        nm[nt][j & 1] = fmaxf(nm[nt][j & 1], v);
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int row = 16 * mt + 8 * hf + ka;
+                        const bool gone = (bad >> (row >> piece_shift)) & 1u;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                if (p0 + row > lim[nt][j] || gone) sc[mt][nt][2 * hf + j] = -INFINITY;
                     }
             }
-            bool moved = false;
+            float top[NT][2];
+            bool over = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
+                    float v = fmaxf(sc[0][nt][j], sc[0][nt][2 + j]);
 #pragma unroll
-                    for (int q = 4; q < 32; q <<= 1) nm[nt][j] = fmaxf(nm[nt][j], __shfl_xor_sync(~0u, nm[nt][j], q));
-                    moved = moved || nm[nt][j] != m[nt][j];
+                    for (int mt = 1; mt < kHalfTiles; ++mt) v = fmaxf(v, fmaxf(sc[mt][nt][j], sc[mt][nt][2 + j]));
+                    top[nt][j] = v;
+                    over = over || fmaf(v, mul[nt][j], shift[nt][j]) > kPShift + kSlack;
                 }
-            if (__any_sync(~0u, moved)) {
+            if (__any_sync(~0u, over)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float al[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        al[j] = nm[nt][j] == m[nt][j] ? 1.0f : exp2_approx(m[nt][j] - nm[nt][j]);
-                        m[nt][j] = nm[nt][j];
+                        float v = top[nt][j];
+#pragma unroll
+                        for (int q = 4; q < 32; q <<= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, q));
+                        v = fmaxf(m[nt][j], v * mul[nt][j]);
+                        al[j] = v == m[nt][j] ? 1.0f : exp2_approx(m[nt][j] - v);
+                        m[nt][j] = v;
+                        shift[nt][j] = v == -INFINITY ? kNone : kPShift - v;
                         ls[nt][j] *= al[j];
                     }
 #pragma unroll
@@ -542,60 +637,58 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __
             }
             uint32_t ph[kHalfTiles][NT][2], pl[kHalfTiles][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float s0 = m[nt][0] == -INFINITY ? 0.0f : kPShift - m[nt][0];
-                const float s1 = m[nt][1] == -INFINITY ? 0.0f : kPShift - m[nt][1];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int mt = 0; mt < kHalfTiles; ++mt)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        const float e0 = exp2_approx(sc[mt][nt][2 * hf] + s0);
-                        const float e1 = exp2_approx(sc[mt][nt][2 * hf + 1] + s1);
+                        const float e0 = exp2_approx(fmaf(sc[mt][nt][2 * hf], mul[nt][0], shift[nt][0]));
+                        const float e1 = exp2_approx(fmaf(sc[mt][nt][2 * hf + 1], mul[nt][1], shift[nt][1]));
                         ls[nt][0] += e0;
                         ls[nt][1] += e1;
                         const uint32_t w = pack_half2(e0, e1);
                         ph[mt][nt][hf] = transpose8(w);
                         if constexpr (SPLIT) pl[mt][nt][hf] = transpose8(pack_rest(e0, e1, w));
                     }
-            }
 
             // --- O^T += V^T P^T
 #pragma unroll
             for (int mt = 0; mt < kHalfTiles; ++mt) {
                 // the lane's four tokens: k indices 2 t4, 2 t4 + 1, and both + 8
-                const int row[4] = {16 * mt + pi8(2 * t4), 16 * mt + pi8(2 * t4 + 1), 16 * mt + 8 + pi8(2 * t4),
-                                    16 * mt + 8 + pi8(2 * t4 + 1)};
                 constexpr int kWords = D / 64;  // words of a lane's D/8 dims
                 uint32_t w[4][kWords];
                 uint32_t sb[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint8_t* v = st + kCodeBytes + row[k] * TL::kRow;
-                    const uint8_t* sv = st + 2 * kCodeBytes + kScaleBytes + row[k] * TL::kBlocks;
+                    const unsigned char* v = st + ((k & 1) ? v_off1 : v_off0) + (16 * mt + 8 * (k >> 1)) * TL::kRow;
+                    const unsigned char* sv = st + ((k & 1) ? vs_off1 : vs_off0) + (16 * mt + 8 * (k >> 1)) * TL::kBlocks;
                     if constexpr (D == 256) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(v + ((2 * g) ^ kv4_swizzle(row[k], TL::kBlocks)) * 8);
+                        const uint4 u = *reinterpret_cast<const uint4*>(v);
                         w[k][0] = u.x, w[k][1] = u.y, w[k][2] = u.z, w[k][3] = u.w;
-                        sb[k] = *reinterpret_cast<const uint16_t*>(sv + 2 * g);
+                        sb[k] = *reinterpret_cast<const uint16_t*>(sv);
                     } else if constexpr (D == 128) {
-                        const uint2 u = *reinterpret_cast<const uint2*>(v + (g ^ kv4_swizzle(row[k], TL::kBlocks)) * 8);
+                        const uint2 u = *reinterpret_cast<const uint2*>(v);
                         w[k][0] = u.x, w[k][1] = u.y;
-                        sb[k] = sv[g];
+                        sb[k] = *sv;
                     } else {
-                        w[k][0] = *reinterpret_cast<const uint32_t*>(v + g * 4);
-                        sb[k] = sv[g >> 1];
+                        w[k][0] = *reinterpret_cast<const uint32_t*>(v);
+                        sb[k] = *sv;
                     }
-                    if (!whole) {
-                        const bool gone = (bad >> (4 * (row[k] >> piece_shift))) & 1u;
-                        if (p0 + row[k] >= x.end || gone) sb[k] = 0;
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = 16 * mt + 8 * (k >> 1) + ((k & 1) ? v1 : v0);
+                        const bool gone = (bad >> (row >> piece_shift)) & 1u;
+                        if (p0 + row >= x.end || gone) sb[k] = 0;
                     }
                 }
                 uint32_t s01 = 0, s23 = 0;
 #pragma unroll
                 for (int wi = 0; wi < kWords; ++wi) {
                     if (wi == 0 || wi == 2) {
-                        const int sh = 8 * (wi / 2);
-                        s01 = ((sb[0] >> sh) & 255u) << 7 | ((sb[1] >> sh) & 255u) << 23;
-                        s23 = ((sb[2] >> sh) & 255u) << 7 | ((sb[3] >> sh) & 255u) << 23;
+                        s01 = scale_both<D>(sb[0], sb[1], wi / 2);
+                        s23 = scale_both<D>(sb[2], sb[3], wi / 2);
                     }
                     uint32_t e01[4], o01[4], e23[4], o23[4];
                     unpack((w[0][wi] & 0x0F0F0F0Fu) | ((w[1][wi] << 4) & 0xF0F0F0F0u), s01, e01);
@@ -614,11 +707,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __
             }
             if (bad != 0 && lane == 0) atomicOr(&g_kv4_attn_error, kErrBadPage);
             ++used;
+            freed = static_cast<int>(s);
+            owed = true;
             __syncwarp();  // every lane has read the stage
-            issue();
         }
 
-        // --- join the warps
+        // --- join the warps: each puts its sums, 8 columns at a time, where its last tile was
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -630,43 +724,44 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __
                     col_l[warp * kCols + 8 * nt + 2 * t4 + j] = ls[nt][j];
                 }
             }
+        if (lane == 0) red_s[warp] = freed;
         __syncthreads();
         const bool done = r0 == 0 && r1 == cur.rounds;
         float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kCols * (D + 2));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float f[2];
+            if (freed >= 0) {
+                float f[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = 8 * nt + 2 * t4 + j;
-                float mm = col_m[c];
+                for (int j = 0; j < 2; ++j) {
+                    const int c = 8 * nt + 2 * t4 + j;
+                    float mm = col_m[c];
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, col_m[w * kCols + c]);
-                f[j] = m[nt][j] == -INFINITY ? 0.0f : exp2_approx(m[nt][j] - mm);
-            }
-            float* mine = red + warp * 8 * S::kRedStride + 2 * t4 * S::kRedStride + 2 * g;
+                    for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, col_m[w * kCols + c]);
+                    f[j] = m[nt][j] == -INFINITY ? 0.0f : exp2_approx(m[nt][j] - mm);
+                }
+                float* mine = reinterpret_cast<float*>(ring + freed * TL::kBytes) + 2 * t4 * S::kRedStride + 2 * g;
 #pragma unroll
-            for (int i = 0; i < kMTiles; ++i) {
-                *reinterpret_cast<float2*>(mine + 16 * i) = make_float2(o[i][nt][0] * f[0], o[i][nt][2] * f[0]);
-                *reinterpret_cast<float2*>(mine + S::kRedStride + 16 * i) = make_float2(o[i][nt][1] * f[1], o[i][nt][3] * f[1]);
+                for (int i = 0; i < kMTiles; ++i) {
+                    *reinterpret_cast<float2*>(mine + 16 * i) = make_float2(o[i][nt][0] * f[0], o[i][nt][2] * f[0]);
+                    *reinterpret_cast<float2*>(mine + S::kRedStride + 16 * i) = make_float2(o[i][nt][1] * f[1], o[i][nt][3] * f[1]);
+                }
             }
             __syncthreads();
             for (int e = tid; e < 8 * D / 2; e += kAttnThreads) {
                 const int c8 = e / (D / 2), pos = 2 * (e % (D / 2)), c = 8 * nt + c8;
                 if (c >= all_cols) continue;
                 float2 v = make_float2(0.0f, 0.0f);
+                float mm = -INFINITY, l = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, col_m[w * kCols + c]);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float2 y = *reinterpret_cast<const float2*>(red + (w * 8 + c8) * S::kRedStride + pos);
+                    if (red_s[w] < 0) continue;
+                    const float* theirs = reinterpret_cast<const float*>(sm + (w * kStages + red_s[w]) * TL::kBytes);
+                    const float2 y = *reinterpret_cast<const float2*>(theirs + c8 * S::kRedStride + pos);
                     v.x += y.x;
                     v.y += y.y;
-                }
-                float mm = col_m[c];
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, col_m[w * kCols + c]);
-                float l = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
                     const float mw = col_m[w * kCols + c];
                     l += col_l[w * kCols + c] * (mw == -INFINITY ? 0.0f : exp2_approx(mw - mm));
                 }
@@ -683,18 +778,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attention_kernel(const __
             }
             __syncthreads();
         }
+        if (owed) issue();
 
         // --- the next unit
         cur.r = r1 - 1;
         cur.left -= r1 - r0 - 1;
         advance<D>(p.c, units, cur);
-    }
-    if (failed) {
-        if (lane == 0) atomicOr(&g_kv4_attn_error, kErrWaitTimeout);
-        while (used < issued) {
-            mbar_wait_bounded(bars + 8 * (used % kStages), (used / kStages) & 1u);
-            ++used;
-        }
     }
 }
 
@@ -705,42 +794,31 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ A
     constexpr size_t kSlot = kCols * (D + 2);
     __shared__ float2 sums[128];
     __shared__ float lsum[128];
-    const int lane = threadIdx.x & 31, c = blockIdx.y, n = gridDim.x;
+    const int lane = threadIdx.x & 31, c = blockIdx.y;
     const int units = p.c.L * p.c.kv_heads * p.col_blocks;
     const long long total = all_rounds<D>(p.c, lane) * units;
+    const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+    griddep_wait();
+    if (static_cast<int>(blockIdx.x) >= n) return;
     long long lo, hi;
     cta_range(total, blockIdx.x, n, lo, hi);
-    griddep_wait();
-    if (lo == hi) return;
     // the unit that this CTA's last round belongs to, if it starts here and ends elsewhere
     Cursor k = locate<D>(p.c, units, hi - 1, lane);
     const long long first = hi - 1 - k.r, end = first + k.rounds;
     if (first < lo || end <= hi) return;
     const Unit x = unit_of(p, k.b, k.u, kCols);
     if (c >= min(x.n * p.group - x.col0, kCols)) return;
-    int last = blockIdx.x;
-    while (hi < end) {
-        ++last;
-        cta_range(total, last, n, lo, hi);
-    }
-    const int parts = last - static_cast<int>(blockIdx.x) + 1;
+    const int parts = cta_of(total, end - 1, n) - static_cast<int>(blockIdx.x) + 1;
     const float* base = p.part + static_cast<size_t>(blockIdx.x) * 2 * kSlot;
     auto slot = [&](int i) -> const float* { return i == 0 ? base + kSlot : base + static_cast<size_t>(i) * 2 * kSlot; };
-    auto empty = [&](int i) -> bool {
-        long long a, z;
-        cta_range(total, blockIdx.x + i, n, a, z);
-        return a == z;
-    };
     float mm = -INFINITY;
-    for (int i = lane; i < parts; i += 32)
-        if (!empty(i)) mm = fmaxf(mm, slot(i)[kCols * D + c]);
+    for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, slot(i)[kCols * D + c]);
     for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
     constexpr int kPairs = D / 2, kWays = 128 / kPairs;
     const int pair = threadIdx.x % kPairs, way = threadIdx.x / kPairs;
     float2 v = make_float2(0.0f, 0.0f);
     float l = 0.0f;
     for (int i = way; i < parts; i += kWays) {
-        if (empty(i)) continue;
         const float* s = slot(i);
         const float ms = s[kCols * D + c];
         const float f = ms == -INFINITY ? 0.0f : exp2_approx(ms - mm);
@@ -772,7 +850,7 @@ int column_tiles(int T, int group, int head_dim) {
     return 4;
 }
 
-constexpr int kMaxCtas = 2 * 192;  // the workspace is sized for cards of up to 192 SMs
+constexpr int kMaxCtas = 4 * 192;  // the workspace is sized for cards of up to 192 SMs
 
 template <int D, int NT, bool SPLIT>
 cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
@@ -789,13 +867,22 @@ cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
     }
-    const int fit = 2 * (S::kBytes + 1024) <= 233472 ? 2 : 1;  // CTAs per SM that shared memory allows
-    const int ctas = std::min(fit * sms, kMaxCtas);
+    constexpr int kFit = Shape<D, NT, SPLIT>::kCtas;
+    static_assert(kFit * (S::kBytes + 1024) <= 233472, "the CTAs of an SM fit its shared memory");
+    const int ctas = std::min(kFit * sms, kMaxCtas);
     kv4_attention_kernel<D, NT, SPLIT><<<ctas, kAttnThreads, S::kBytes, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    kv4_join_kernel<D, NT><<<dim3(ctas, 8 * NT), 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, 8 * NT);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, p);
 }
 
 template <int D, int NT>
