@@ -87,64 +87,80 @@ struct AttnParams {
 __device__ __forceinline__ int pi8(int r) { return r ^ ((r >> 1) & 1); }
 
 // ------------------------------------------------------------ work split --
-// Rounds of one unit of sequence b.
+// The units lie end to end on a line: each takes kUnitCost places for its start (its queries are read, its
+// warps joined) and then one per round. CTA i of n has the places [total i / n, total (i + 1) / n) and does the
+// rounds among them. Without the places for starts a CTA of 20 rounds could get 20 one-round sequences: a batch of
+// 64 sequences of mixed lengths up to 8192 took 61 us so, 46 us with them.
+constexpr int kUnitCost = 2;
+
+// Places of one unit of sequence b (0: no token).
 template <int D>
-__device__ __forceinline__ int seq_rounds(const Kv4Cache& c, int b) {
+__device__ __forceinline__ int seq_cost(const Kv4Cache& c, int b) {
     const Kv4Window w = kv4_window(c, b);
     if (w.n == 0) return 0;
-    const int end = min(w.start + min(w.n, w.cap - w.start), w.cap);
+    const int end = w.start + min(w.n, w.cap - w.start);
     constexpr int kRound = Tile<D>::kTokens * kWarps;
-    return (end + kRound - 1) / kRound;
+    return kUnitCost + (end + kRound - 1) / kRound;
 }
 
+// Where a CTA is: unit u of sequence b (cost places long), at place `at` of it, with `left` places to go.
 struct Cursor {
-    int b, u, r, rounds;
-    long long left;  // rounds still to do in this CTA, this one included
+    int b, u, cost, at;
+    long long left;
 };
 
-// Rounds [lo, hi) of CTA i of n <= total: each has one at least.
-__device__ __forceinline__ void cta_range(long long total, int i, int n, long long& lo, long long& hi) {
-    lo = total * i / n;
-    hi = total * (i + 1) / n;
+// a b / c, in 32 bits where they suffice.
+__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
+    const unsigned long long x = static_cast<unsigned long long>(a) * b;
+    if ((x | static_cast<unsigned long long>(c)) >> 32) return x / static_cast<unsigned long long>(c);
+    return static_cast<uint32_t>(x) / static_cast<uint32_t>(c);
 }
 
-// The CTA of n that has round x: the largest i with total i / n <= x.
+// Places [lo, hi) of CTA i of n <= total: each has one at least.
+__device__ __forceinline__ void cta_range(long long total, int i, int n, long long& lo, long long& hi) {
+    lo = mul_div(total, i, n);
+    hi = mul_div(total, i + 1, n);
+}
+
+// The CTA of n that has place x: the largest i with total i / n <= x.
 __device__ __forceinline__ int cta_of(long long total, long long x, int n) {
     return static_cast<int>(((x + 1) * n - 1) / total);
 }
 
-// Sum of the sequences' rounds, by one warp.
+// Places of all sequences' units (of one unit each), by one warp.
 template <int D>
-__device__ __forceinline__ long long all_rounds(const Kv4Cache& c, int lane) {
+__device__ __forceinline__ long long all_costs(const Kv4Cache& c, int lane) {
     long long s = 0;
-    for (int b = lane; b < c.B; b += 32) s += seq_rounds<D>(c, b);
+    for (int b = lane; b < c.B; b += 32) s += seq_cost<D>(c, b);
+    if (c.B == 1) return __shfl_sync(~0u, s, 0);
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
     return s;
 }
 
-// The unit and round that global round `at` belongs to (units per sequence: `units`), by one warp.
+// The unit and place in it of place x of the line (units per sequence: `units`), by one warp.
 template <int D>
-__device__ __forceinline__ Cursor locate(const Kv4Cache& c, int units, long long at, int lane) {
+__device__ __forceinline__ Cursor locate(const Kv4Cache& c, int units, long long x, int lane) {
     Cursor k;
     k.b = c.B;
-    k.u = k.r = k.rounds = 0;
+    k.u = k.cost = k.at = 0;
     k.left = 0;
     long long before = 0;
     for (int b0 = 0; b0 < c.B; b0 += 32) {
-        const int mine = b0 + lane < c.B ? seq_rounds<D>(c, b0 + lane) : 0;
+        const int mine = b0 + lane < c.B ? seq_cost<D>(c, b0 + lane) : 0;
         int sum = mine;
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(~0u, sum, o);
             if (lane >= o) sum += v;
         }
-        const unsigned hit = __ballot_sync(~0u, (before + sum) * units > at);
+        const unsigned hit = __ballot_sync(~0u, (before + sum) * units > x);
         if (hit != 0) {
             const int src = __ffs(hit) - 1;
             k.b = b0 + src;
-            k.rounds = __shfl_sync(~0u, mine, src);
-            const long long base = (before + __shfl_sync(~0u, sum, src) - k.rounds) * units;
-            k.u = static_cast<int>((at - base) / k.rounds);
-            k.r = static_cast<int>((at - base) - static_cast<long long>(k.u) * k.rounds);
+            k.cost = __shfl_sync(~0u, mine, src);
+            const long long base = (before + __shfl_sync(~0u, sum, src) - k.cost) * units;
+            k.u = static_cast<int>(mul_div(x - base, 1, k.cost));
+            k.at = static_cast<int>((x - base) - static_cast<long long>(k.u) * k.cost);
             return k;
         }
         before += __shfl_sync(~0u, sum, 31);
@@ -152,16 +168,22 @@ __device__ __forceinline__ Cursor locate(const Kv4Cache& c, int units, long long
     return k;
 }
 
+// The rounds [r0, r1) of the cursor's unit that are its CTA's.
+__device__ __forceinline__ void unit_rounds(const Cursor& k, int& r0, int& r1) {
+    r0 = max(k.at - kUnitCost, 0);
+    r1 = static_cast<int>(min(static_cast<long long>(k.cost), k.at + k.left)) - kUnitCost;
+}
+
+// On to the next unit.
 template <int D>
 __device__ __forceinline__ void advance(const Kv4Cache& c, int units, Cursor& k) {
-    --k.left;
-    if (++k.r < k.rounds) return;
-    k.r = 0;
-    if (++k.u < units) return;
+    k.left -= k.cost - k.at;
+    k.at = 0;
+    if (++k.u < units || k.left <= 0) return;
     k.u = 0;
     do {
         ++k.b;
-    } while (k.b < c.B && (k.rounds = seq_rounds<D>(c, k.b)) == 0);
+    } while (k.b < c.B && (k.cost = seq_cost<D>(c, k.b)) == 0);
 }
 
 // A unit: its layer, kv head, first column, and the positions its columns see.
@@ -245,6 +267,14 @@ __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
     return pack_half2(a - f.x, b - f.y);
 }
 
+constexpr float kLeastScale = 1.17549435e-38f;  // the factor of raw scores is never 0: 0 times a masked -inf
+
+// 2^(11 - exponent of a row's largest magnitude): scaled by it the row fills fp16's range, exactly.
+__device__ __forceinline__ float row_factor(float a) {
+    const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -115), 127);
+    return a > 0.0f && a <= 3.0e38f ? __uint_as_float(static_cast<uint32_t>(138 - e) << 23) : 1.0f;
+}
+
 __device__ __forceinline__ float4 load_q4(const AttnParams& p, size_t i) {
     if (p.dtype == DType::kF32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + i);
     const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + i);
@@ -270,7 +300,7 @@ __device__ __forceinline__ void store_out2(const AttnParams& p, size_t i, float 
 
 // Row (t, query head) of column col of a unit: its first element in q and out.
 __device__ __forceinline__ size_t q_row(const AttnParams& p, int b, const Unit& x, int col) {
-    const int t = col / p.group;
+    const int t = p.c.T == 1 ? 0 : col / p.group;
     const int head = x.h * p.group + (col - t * p.group);
     return (((static_cast<size_t>(b) * p.c.L + x.l) * p.c.T + t) * p.q_heads + head) * p.c.head_dim;
 }
@@ -324,7 +354,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
     int* red_s = reinterpret_cast<int*>(sm + S::kOffRed);
     unsigned char* ring = sm + warp * kStages * TL::kBytes;
     const int units = p.c.L * p.c.kv_heads * p.col_blocks;
-    const long long total = all_rounds<D>(p.c, lane) * units;
+    const long long total = all_costs<D>(p.c, lane) * units;
     const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
     if (static_cast<int>(blockIdx.x) >= ctas) return;
     long long lo, hi;
@@ -358,10 +388,10 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
             a_end = u.end;
             a_head = p.c.cache + (static_cast<size_t>(u.l) * p.c.n_pages * p.c.kv_heads + u.h) * head_bytes;
             a_table = p.c.block_table + static_cast<size_t>(ahead.b) * p.c.max_pages;
-            a_seg = static_cast<int>(min(static_cast<long long>(ahead.rounds - ahead.r), ahead.left));
-            a_p0 = ahead.r * kRound + warp * kTokens;
-            ahead.r += a_seg - 1;
-            ahead.left -= a_seg - 1;
+            int r0, r1;
+            unit_rounds(ahead, r0, r1);
+            a_seg = r1 - r0;
+            a_p0 = r0 * kRound + warp * kTokens;
             advance<D>(p.c, units, ahead);
         }
         ready = true;
@@ -448,48 +478,63 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
     while (cur.left > 0) {
         const Unit x = unit_of(p, cur.b, cur.u, kCols);
         const int b = cur.b;
-        const int r0 = cur.r;
-        const int r1 = static_cast<int>(min(static_cast<long long>(cur.rounds), r0 + cur.left));
+        int r0, r1;
+        unit_rounds(cur, r0, r1);
+        if (r1 <= r0) break;  // its start alone, at the end of the CTA's places
 
-        // --- queries of the unit: B fragments in shared memory
-        __syncthreads();
+        // --- queries of the unit: B fragments in shared memory, or straight in registers
         const int all_cols = min(x.n * p.group - x.col0, kCols);  // columns that exist (<= 0: none)
         if (tid == 0 && x.n > kv4_window(p.c, b).cap - x.start) atomicOr(&g_kv4_attn_error, kErrBadPage);
-        for (int c = warp; c < kCols; c += kWarps) {
-            constexpr int kChunks = D > 128 ? D / 128 : 1;
-            float4 v[kChunks];
+        uint2 qr[kQRegs ? D / 16 : 1];
+        float col_mul = 0.0f;  // of column g
+        if constexpr (kQRegs) {
+            constexpr int kSpan = D / 4;  // contiguous dims of a lane
+            float4 v[D / 16];
             float a = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
+            for (int i = 0; i < D / 16; ++i) {
                 v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (c < all_cols && 4 * lane + 128 * i < D) v[i] = load_q4(p, q_row(p, b, x, x.col0 + c) + 128 * i + 4 * lane);
+                if (g < all_cols) v[i] = load_q4(p, q_row(p, b, x, x.col0 + g) + kSpan * t4 + 4 * i);
                 a = fmaxf(fmaxf(a, fmaxf(fabsf(v[i].x), fabsf(v[i].y))), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
             }
+            a = fmaxf(a, __shfl_xor_sync(~0u, a, 1));
+            a = fmaxf(a, __shfl_xor_sync(~0u, a, 2));
+            const float f = row_factor(a);
+            col_mul = fmaxf(p.scale_log2 / f, kLeastScale);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
-            // f = 2^(11 - exponent of the largest magnitude): the row fills fp16's range, exactly
-            const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -115), 127);
-            const float f = a > 0.0f && a <= 3.0e38f ? __uint_as_float(static_cast<uint32_t>(138 - e) << 23) : 1.0f;
-            if (lane == 0) mul_s[c] = fmaxf(p.scale_log2 / f, 1.17549435e-38f);  // never 0: 0 times a masked -inf
+            for (int i = 0; i < D / 16; ++i)
+                qr[i] = make_uint2(pack_half2(v[i].x * f, v[i].y * f), pack_half2(v[i].z * f, v[i].w * f));
+        } else {
+            __syncthreads();
+            for (int c = warp; c < kCols; c += kWarps) {
+                constexpr int kChunks = D > 128 ? D / 128 : 1;
+                float4 v[kChunks];
+                float a = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                if (4 * lane + 128 * i >= D) continue;
-                constexpr int kPerT4 = D >= 128 ? 8 : 4;  // k-steps of a lane's contiguous dims
-                const int st = 8 * i + (lane & (kPerT4 - 1)), tt = lane / kPerT4;
-                const float q0 = v[i].x * f, q1 = v[i].y * f, q2 = v[i].z * f, q3 = v[i].w * f;
-                const uint32_t at = ((st * NT + (c >> 3)) * 32 + (c & 7) * 4 + tt) * 8;
-                uint2 w = make_uint2(pack_half2(q0, q1), pack_half2(q2, q3));
-                *reinterpret_cast<uint2*>(sm + S::kOffQ + at) = w;
-                if constexpr (SPLIT)
-                    *reinterpret_cast<uint2*>(sm + S::kOffQ + kCols * D * 2 + at) =
-                        make_uint2(pack_rest(q0, q1, w.x), pack_rest(q2, q3, w.y));
+                for (int i = 0; i < kChunks; ++i) {
+                    v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (c < all_cols && 4 * lane + 128 * i < D) v[i] = load_q4(p, q_row(p, b, x, x.col0 + c) + 128 * i + 4 * lane);
+                    a = fmaxf(fmaxf(a, fmaxf(fabsf(v[i].x), fabsf(v[i].y))), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
+                const float f = row_factor(a);
+                if (lane == 0) mul_s[c] = fmaxf(p.scale_log2 / f, kLeastScale);
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    if (4 * lane + 128 * i >= D) continue;
+                    constexpr int kPerT4 = D >= 128 ? 8 : 4;  // k-steps of a lane's contiguous dims
+                    const int st = 8 * i + (lane & (kPerT4 - 1)), tt = lane / kPerT4;
+                    const float q0 = v[i].x * f, q1 = v[i].y * f, q2 = v[i].z * f, q3 = v[i].w * f;
+                    const uint32_t at = ((st * NT + (c >> 3)) * 32 + (c & 7) * 4 + tt) * 8;
+                    uint2 w = make_uint2(pack_half2(q0, q1), pack_half2(q2, q3));
+                    *reinterpret_cast<uint2*>(sm + S::kOffQ + at) = w;
+                    if constexpr (SPLIT)
+                        *reinterpret_cast<uint2*>(sm + S::kOffQ + kCols * D * 2 + at) =
+                            make_uint2(pack_rest(q0, q1, w.x), pack_rest(q2, q3, w.y));
+                }
             }
-        }
-        __syncthreads();
-        uint2 qr[kQRegs ? D / 16 : 1];
-        if constexpr (kQRegs) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) qr[i] = *reinterpret_cast<const uint2*>(sm + S::kOffQ + (i * 32 + lane) * 8);
+            __syncthreads();
         }
 
         float m[NT][2], shift[NT][2], ls[NT][2], mul[NT][2];
@@ -503,7 +548,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
                 m[nt][j] = -INFINITY;
                 shift[nt][j] = kNone;
                 ls[nt][j] = 0.0f;
-                mul[nt][j] = mul_s[c];
+                mul[nt][j] = kQRegs ? __shfl_sync(~0u, col_mul, (c & 7) * 4) : mul_s[c];
                 lim[nt][j] = c < all_cols ? min(x.start + (x.col0 + c) / p.group, x.end - 1) : -1;
             }
 #pragma unroll
@@ -726,7 +771,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
             }
         if (lane == 0) red_s[warp] = freed;
         __syncthreads();
-        const bool done = r0 == 0 && r1 == cur.rounds;
+        const bool done = r0 == 0 && r1 == cur.cost - kUnitCost;
         float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kCols * (D + 2));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -781,8 +826,6 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
         if (owed) issue();
 
         // --- the next unit
-        cur.r = r1 - 1;
-        cur.left -= r1 - r0 - 1;
         advance<D>(p.c, units, cur);
     }
 }
@@ -796,16 +839,20 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ A
     __shared__ float lsum[128];
     const int lane = threadIdx.x & 31, c = blockIdx.y;
     const int units = p.c.L * p.c.kv_heads * p.col_blocks;
-    const long long total = all_rounds<D>(p.c, lane) * units;
+    const long long total = all_costs<D>(p.c, lane) * units;
     const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-    griddep_wait();
-    if (static_cast<int>(blockIdx.x) >= n) return;
-    long long lo, hi;
-    cta_range(total, blockIdx.x, n, lo, hi);
-    // the unit that this CTA's last round belongs to, if it starts here and ends elsewhere
-    Cursor k = locate<D>(p.c, units, hi - 1, lane);
-    const long long first = hi - 1 - k.r, end = first + k.rounds;
-    if (first < lo || end <= hi) return;
+    long long lo = 0, hi = 0, first = 0, end = 0;
+    Cursor k{};
+    bool mine = false;  // the unit that this CTA's last place belongs to has rounds that start here and end elsewhere
+    if (static_cast<int>(blockIdx.x) < n) {
+        cta_range(total, blockIdx.x, n, lo, hi);
+        k = locate<D>(p.c, units, hi - 1, lane);
+        first = hi - 1 - k.at;
+        end = first + k.cost;
+        mine = first + kUnitCost >= lo && k.at >= kUnitCost && end > hi;
+    }
+    griddep_wait();  // in every block: the grid must not end before the one it follows
+    if (!mine) return;
     const Unit x = unit_of(p, k.b, k.u, kCols);
     if (c >= min(x.n * p.group - x.col0, kCols)) return;
     const int parts = cta_of(total, end - 1, n) - static_cast<int>(blockIdx.x) + 1;
