@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = ["gdn_step.cu", "gdn_decode_t1.cu", "gdn_chunk.cu", "gdn_window_tc.cu", "gdn_ab.cu", "gdn_proj.cu", "gdn_proj_noalloc.cu", "gdn_host_pipeline.cpp", "gdn_api.cpp",
-           "gdn_kv4_cache.cu", "gdn_kv4_attention.cu", "gdn_logprobs.cu", "gdn_ops_api.cpp"]
+           "gdn_kv4_cache.cu", "gdn_kv4_attention.cu", "gdn_kv4_window.cu", "gdn_logprobs.cu", "gdn_ops_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # A standalone measuring program, not linked into the library: the device's FP32 FMA rate.
 FMA_RATE_SRC = "fp32_fma_rate.cu"

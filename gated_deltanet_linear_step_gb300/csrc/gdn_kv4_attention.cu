@@ -48,7 +48,7 @@
 #include <atomic>
 
 #include "gdn_device.cuh"
-#include "gdn_kv4.cuh"
+#include "gdn_kv4_attention.cuh"
 #include "gdn_tc.cuh"
 
 namespace gdn {
@@ -56,9 +56,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kAttnThreads = 32 * kWarps;
-constexpr float kPShift = 8.0f;  // probabilities are kept relative to 2^-8 of the reference maximum ...
-constexpr float kSlack = 6.0f;   // ... which is raised when a score exceeds it by 6: none is above 2^14
-constexpr float kNone = 1e30f;   // the shift of a column that has seen no key
 
 __device__ unsigned int g_kv4_attn_error = 0;
 
@@ -71,16 +68,6 @@ struct Tile {
     static constexpr uint32_t kCodeBytes = kTokens * kRow;
     static constexpr uint32_t kScaleBytes = kTokens * kBlocks;
     static constexpr uint32_t kBytes = 2 * (kCodeBytes + kScaleBytes);
-};
-
-struct AttnParams {
-    Kv4Cache c;
-    const void* q;
-    void* out;
-    float* part;  // per CTA two partial results: [columns][D] sums, then maxima and sums of the columns
-    int q_heads, group, col_blocks;
-    DType dtype;
-    float scale_log2;
 };
 
 // Token of row r of an 8-row half tile.
@@ -108,24 +95,6 @@ struct Cursor {
     int b, u, cost, at;
     long long left;
 };
-
-// a b / c, in 32 bits where they suffice.
-__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
-    const unsigned long long x = static_cast<unsigned long long>(a) * b;
-    if ((x | static_cast<unsigned long long>(c)) >> 32) return x / static_cast<unsigned long long>(c);
-    return static_cast<uint32_t>(x) / static_cast<uint32_t>(c);
-}
-
-// Places [lo, hi) of CTA i of n <= total: each has one at least.
-__device__ __forceinline__ void cta_range(long long total, int i, int n, long long& lo, long long& hi) {
-    lo = mul_div(total, i, n);
-    hi = mul_div(total, i + 1, n);
-}
-
-// The CTA of n that has place x: the largest i with total i / n <= x.
-__device__ __forceinline__ int cta_of(long long total, long long x, int n) {
-    return static_cast<int>(((x + 1) * n - 1) / total);
-}
 
 // Places of all sequences' units (of one unit each), by one warp.
 template <int D>
@@ -186,11 +155,6 @@ __device__ __forceinline__ void advance(const Kv4Cache& c, int units, Cursor& k)
     } while (k.b < c.B && (k.cost = seq_cost<D>(c, k.b)) == 0);
 }
 
-// A unit: its layer, kv head, first column, and the positions its columns see.
-struct Unit {
-    int l, h, col0, start, n, end;  // end: first position that no column sees
-};
-
 __device__ __forceinline__ Unit unit_of(const AttnParams& p, int b, int u, int columns) {
     Unit x;
     const int qb = u % p.col_blocks;
@@ -228,81 +192,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     return r;
 }
 
-// The 8 codes of a word as four fp16 pairs, times a pair of scales.
-__device__ __forceinline__ void unpack(uint32_t w, uint32_t s, uint32_t (&v)[4]) {
-    asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
-        "mov.b32 {c0, c1, c2, c3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, c0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, c1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, c3;\n\t}"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-        : "r"(w));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(s));
-}
-
-// Byte i (0 or 1) of a as both halves of an fp16 pair of scales, and byte i of a and of b as its halves.
-__device__ __forceinline__ uint32_t scale_twice(uint32_t a, int i) { return __byte_perm(a, 0, i ? 0x4141 : 0x4040) << 7; }
+// Byte i (0 or 1) of a and of b as the halves of an fp16 pair of scales.
 template <int D>
 __device__ __forceinline__ uint32_t scale_both(uint32_t a, uint32_t b, int i) {
     if constexpr (D < 256) return __byte_perm(a, b, 0x5410) << 7;  // a and b have one byte each
     return (__byte_perm(a, b, i ? 0x5511 : 0x4400) & 0x00FF00FFu) << 7;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// What rounding to fp16 left of two floats, rounded to fp16.
-__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    return pack_half2(a - f.x, b - f.y);
-}
-
-constexpr float kLeastScale = 1.17549435e-38f;  // the factor of raw scores is never 0: 0 times a masked -inf
-
-// 2^(11 - exponent of a row's largest magnitude): scaled by it the row fills fp16's range, exactly.
-__device__ __forceinline__ float row_factor(float a) {
-    const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -115), 127);
-    return a > 0.0f && a <= 3.0e38f ? __uint_as_float(static_cast<uint32_t>(138 - e) << 23) : 1.0f;
-}
-
-__device__ __forceinline__ float4 load_q4(const AttnParams& p, size_t i) {
-    if (p.dtype == DType::kF32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + i);
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + i);
-    if (p.dtype == DType::kF16) {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-        return make_float4(a.x, a.y, b.x, b.y);
-    }
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xFFFF0000u));
-}
-
-__device__ __forceinline__ void store_out2(const AttnParams& p, size_t i, float a, float b) {
-    if (p.dtype == DType::kF32) {
-        *reinterpret_cast<float2*>(static_cast<float*>(p.out) + i) = make_float2(a, b);
-    } else if (p.dtype == DType::kF16) {
-        *reinterpret_cast<uint32_t*>(static_cast<__half*>(p.out) + i) = pack_half2(a, b);
-    } else {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + i) = *reinterpret_cast<const uint32_t*>(&v);
-    }
-}
-
-// Row (t, query head) of column col of a unit: its first element in q and out.
-__device__ __forceinline__ size_t q_row(const AttnParams& p, int b, const Unit& x, int col) {
-    const int t = p.c.T == 1 ? 0 : col / p.group;
-    const int head = x.h * p.group + (col - t * p.group);
-    return (((static_cast<size_t>(b) * p.c.L + x.l) * p.c.T + t) * p.q_heads + head) * p.c.head_dim;
 }
 
 // Output sums lie permuted: pair (i, g) of the dims (D/8) g + 2 i + {0, 1} is at 16 i + 2 g.
@@ -887,15 +781,12 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ A
     store_out2(p, q_row(p, k.b, x, x.col0 + c) + dim_of<D>(2 * pair), v.x * inv, v.y * inv);
 }
 
-// 8-column tiles per block: as few as hold the window's columns, at most 4 (2 at D = 256), where
-// the accumulators end.
-int column_tiles(int T, int group, int head_dim) {
-    const long long cols = static_cast<long long>(T) * group;
-    const int most = head_dim == 256 ? 2 : 4;
-    if (cols <= 8) return 1;
-    if (cols <= 16 || most == 2) return 2;
-    return 4;
-}
+// Windows of more query rows per kv head than this go to the tensor cores (gdn_kv4_window.cu).
+constexpr int kMostColumns = 16;
+
+bool on_tensor_cores(int T, int group) { return static_cast<long long>(T) * group > kMostColumns; }
+
+int column_tiles(int T, int group) { return T * group <= 8 ? 1 : 2; }
 
 constexpr int kMaxCtas = 4 * 192;  // the workspace is sized for cards of up to 192 SMs
 
@@ -940,9 +831,7 @@ cudaError_t launch_split(const AttnParams& p, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_dim(const AttnParams& p, int nt, cudaStream_t stream) {
     if (nt == 1) return launch_split<D, 1>(p, stream);
-    if (nt == 2) return launch_split<D, 2>(p, stream);
-    if constexpr (D < 256) return launch_split<D, 4>(p, stream);
-    return cudaErrorInvalidValue;
+    return launch_split<D, 2>(p, stream);
 }
 
 }  // namespace
@@ -950,7 +839,9 @@ cudaError_t launch_dim(const AttnParams& p, int nt, cudaStream_t stream) {
 size_t kv4_attention_workspace_bytes(int B, int L, int T, int q_heads, int kv_heads, int head_dim) {
     (void)B;
     (void)L;
-    const int nt = column_tiles(T, q_heads / kv_heads, head_dim);
+    const int group = q_heads / kv_heads;
+    if (on_tensor_cores(T, group)) return kv4_window_workspace_bytes(head_dim);
+    const int nt = column_tiles(T, group);
     return static_cast<size_t>(kMaxCtas) * 2 * (8 * nt) * (head_dim + 2) * sizeof(float);
 }
 
@@ -964,7 +855,8 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t stream) {
     p.group = a.q_heads / a.c.kv_heads;
     p.dtype = a.dtype;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    const int nt = column_tiles(a.c.T, p.group, a.c.head_dim);
+    if (on_tensor_cores(a.c.T, p.group)) return launch_kv4_window(p, stream);
+    const int nt = column_tiles(a.c.T, p.group);
     p.col_blocks = static_cast<int>((static_cast<long long>(a.c.T) * p.group + 8 * nt - 1) / (8 * nt));
     switch (a.c.head_dim) {
         case 64: return launch_dim<64>(p, nt, stream);

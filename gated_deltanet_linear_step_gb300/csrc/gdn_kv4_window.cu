@@ -1,0 +1,778 @@
+// gdn_kv4_window.cu - attention over the 4-bit cache for windows with many query
+// rows (verify windows, prompt chunks): the same mathematics as
+// gdn_kv4_attention.cu, on the 5th-generation tensor cores.
+//
+//   S = Q K^T   128 rows x 64 tokens x D,   O += P V   128 rows x D x 64 tokens
+//
+// A row is a (token, query head) pair of one kv head's group, so one unpacked tile of
+// keys and values serves the whole group of a block of tokens. What bounds
+// it for long windows: per 64-token tile and 128 rows (D = 128) the products take 512
+// clocks of an SM's tensor pipe, the 8192 exponentials 512 of its special-function
+// pipe, and unpacking and softmax about 500 issue slots of each of its four schedulers; the roles below
+// overlap the three, and two CTAs per SM (D <= 128) fill each other's waits.
+//
+//   warps 0-3  a row per thread: queries in, the softmax of a tile from tensor
+//              memory, probabilities back to tensor memory (fp16, over the scores they
+//              came from, as the A operand of the second product), outputs out
+//   warps 4-7  unpack the next tiles: 16 bytes of codes per thread from global
+//              memory, a tile ahead in registers, to fp16 in the swizzled
+//              K-major rows that both products read (V with its rows as K: MN-major)
+//   warp 8     issues the products
+//
+// Scores have two buffers in tensor memory, K and V tiles two stages each, so
+// the product of tile j + 1 runs during the softmax of tile j. The
+// running maximum is a reference that is raised only when a score exceeds it by
+// kSlack (in base 2): then the row's sums are read, scaled and written back,
+// which is rare after the first tile. fp32 calls take Q and P as fp16 hi + lo, two products each.
+//
+// Numerics, masks and missing pages: as in gdn_kv4_attention.cu. Tokens past a
+// block's end and those of missing pages are unpacked as zeros.
+//
+// Work split: blocks of 128 rows have different numbers of tiles (causal), so the
+// line that is dealt out to the CTAs has the blocks of each sequence in turn, each times its (layer, kv head) pairs.
+// Waits are bounded; one that gives up makes its role leave its loop, the others run
+// into their own limits, the device error word is set and the tensor memory freed.
+
+#include <algorithm>
+#include <atomic>
+
+#include "gdn_device.cuh"
+#include "gdn_kv4_attention.cuh"
+#include "gdn_tc.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kRows = 128;       // of a block
+constexpr int kTok = 64;         // of a tile
+constexpr int kSoftWarps = 4, kUnpackWarps = 4;
+constexpr int kWinThreads = 32 * (kSoftWarps + kUnpackWarps + 1);
+constexpr int kStartCost = 4;    // places of a block's start on the line, in tiles
+
+__device__ unsigned int g_kv4_window_error = 0;
+
+template <int D, bool SPLIT>
+struct Win {
+    static constexpr int kStages = D == 256 && SPLIT ? 1 : 2;
+    static constexpr int kBlk = D / 64;                        // 64-dim blocks of a row (128 bytes)
+    static constexpr uint32_t kQBlock = kRows * 128;           // bytes of a block of Q
+    static constexpr uint32_t kQBytes = kBlk * kQBlock;        // of Q hi (then lo)
+    static constexpr uint32_t kKvBlock = kTok * 128;           // of a block of K or V
+    static constexpr uint32_t kKvBytes = kBlk * kKvBlock;
+    static constexpr uint32_t kOffK = kQBytes * (SPLIT ? 2 : 1);
+    static constexpr uint32_t kOffV = kOffK + kStages * kKvBytes;
+    static constexpr uint32_t kOffMul = kOffV + kStages * kKvBytes;  // factor of a row's raw scores
+    static constexpr uint32_t kOffBad = kOffMul + kRows * 4;         // missing pages of tiles j mod 4
+    static constexpr uint32_t kOffBar = kOffBad + 4 * 4;
+    static constexpr uint32_t kBars = 2 + 2 + 2 + 2 + 2 + 1 + 1;     // see below
+    static constexpr uint32_t kUsed = kOffBar + kBars * 8 + 64;      // + cursor, tensor memory address
+    static constexpr int kCtas = D <= 128 && 2 * (kUsed + 2048) <= 232448 ? 2 : 1;
+    // no more CTAs than the tensor memory has room for: a third (second) would wait in its allocation
+    static constexpr uint32_t kLeast = kCtas == 2 ? 80 * 1024 : 118 * 1024;
+    static constexpr uint32_t kSmem = (kUsed + 1024 > kLeast ? kUsed + 1024 : kLeast);
+    static constexpr uint32_t kTmCols = D == 256 ? 512 : 256;
+    static constexpr uint32_t kTmO = 128;                            // scores at 0 and 64
+};
+
+// Where a CTA is: unit (b, block, pair of layer and kv head), at place `at` of its `cost`, `left` places to go.
+struct WinCursor {
+    int b, blk, lh, cost, at;
+    int left;
+};
+
+// First position that no row of block blk sees (0: no row).
+__device__ __forceinline__ int block_end(const AttnParams& p, const Kv4Window& w, int blk) {
+    const long long row = static_cast<long long>(blk) * kRows;
+    if (row >= static_cast<long long>(w.n) * p.group) return 0;
+    const int t_hi = static_cast<int>(min((row + kRows - 1) / p.group, static_cast<long long>(w.n) - 1));
+    return w.start + min(t_hi + 1, w.cap - w.start);
+}
+
+__device__ __forceinline__ int block_cost(const AttnParams& p, const Kv4Window& w, int blk) {
+    const int end = block_end(p, w, blk);
+    return end == 0 ? 0 : kStartCost + (end + kTok - 1) / kTok;
+}
+
+// Places of sequence b, of one (layer, kv head) pair.
+__device__ __forceinline__ int seq_cost(const AttnParams& p, int b) {
+    const Kv4Window w = kv4_window(p.c, b);
+    int s = 0;
+    for (int blk = 0; blk < p.col_blocks; ++blk) {
+        const int c = block_cost(p, w, blk);
+        if (c == 0) break;
+        s += c;
+    }
+    return s;
+}
+
+__device__ __forceinline__ long long line_length(const AttnParams& p, int pairs, int lane) {
+    long long s = 0;
+    for (int b = lane; b < p.c.B; b += 32) s += seq_cost(p, b);
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    return s * pairs;
+}
+
+// Inclusive sums over the lanes.
+__device__ __forceinline__ long long scan(long long v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
+
+// The unit and place in it of place x of the line, by one warp.
+__device__ __forceinline__ WinCursor find(const AttnParams& p, int pairs, long long x, int lane) {
+    WinCursor k{p.c.B, 0, 0, 0, 0, 0};
+    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+        const long long mine = b0 + lane < p.c.B ? static_cast<long long>(seq_cost(p, b0 + lane)) * pairs : 0;
+        const long long sum = scan(mine, lane);
+        const unsigned hit = __ballot_sync(~0u, sum > x);
+        if (hit == 0) {
+            x -= __shfl_sync(~0u, sum, 31);
+            continue;
+        }
+        const int src = __ffs(hit) - 1;
+        k.b = b0 + src;
+        x -= __shfl_sync(~0u, sum - mine, src);
+        const Kv4Window w = kv4_window(p.c, k.b);
+        for (int m0 = 0; m0 < p.col_blocks; m0 += 32) {
+            const int cost = m0 + lane < p.col_blocks ? block_cost(p, w, m0 + lane) : 0;
+            const long long of_block = scan(static_cast<long long>(cost) * pairs, lane);
+            const unsigned at = __ballot_sync(~0u, of_block > x);
+            if (at == 0) {
+                x -= __shfl_sync(~0u, of_block, 31);
+                continue;
+            }
+            const int bl = __ffs(at) - 1;
+            k.blk = m0 + bl;
+            k.cost = __shfl_sync(~0u, cost, bl);
+            x -= __shfl_sync(~0u, of_block, bl) - static_cast<long long>(k.cost) * pairs;
+            k.lh = static_cast<int>(mul_div(x, 1, k.cost));
+            k.at = static_cast<int>(x - static_cast<long long>(k.lh) * k.cost);
+            return k;
+        }
+        return k;
+    }
+    return k;
+}
+
+__device__ __forceinline__ void next_unit(const AttnParams& p, int pairs, WinCursor& k) {
+    k.left -= k.cost - k.at;
+    k.at = 0;
+    if (++k.lh < pairs || k.left <= 0) return;
+    k.lh = 0;
+    ++k.blk;
+    while (k.b < p.c.B) {
+        if (k.blk < p.col_blocks && (k.cost = block_cost(p, kv4_window(p.c, k.b), k.blk)) > 0) return;
+        k.blk = 0;
+        ++k.b;
+    }
+}
+
+// The tiles [r0, r1) of the cursor's unit that are its CTA's.
+__device__ __forceinline__ void unit_tiles(const WinCursor& k, int& r0, int& r1) {
+    r0 = max(k.at - kStartCost, 0);
+    r1 = min(k.cost, k.at + k.left) - kStartCost;
+}
+
+__device__ __forceinline__ Unit win_unit(const AttnParams& p, const WinCursor& k) {
+    Unit x;
+    const Kv4Window w = kv4_window(p.c, k.b);
+    x.h = k.lh % p.c.kv_heads;
+    x.l = k.lh / p.c.kv_heads;
+    x.col0 = k.blk * kRows;
+    x.start = w.start;
+    x.n = w.n;
+    x.end = block_end(p, w, k.blk);
+    return x;
+}
+
+// fp16 by fp16, fp32 accumulation, M = 128.
+__host__ __device__ constexpr uint32_t idesc_f16(int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+
+// A from tensor memory (fp16 pairs, 8 columns of 32 bits per k-step of 16).
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 consecutive columns of this warp's lanes, one lane per thread, complete when it returns.
+__device__ __forceinline__ void tmem_read32(uint32_t taddr, float (&v)[32]) {
+    uint32_t u[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+          "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+}
+
+// Stores 16 consecutive columns of this warp's lanes, one lane per thread.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// Every lane of a warp waits; false, for all of them, if one gave up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    const bool late = !mbar_wait_bounded(bar, parity);
+    return !__any_sync(~0u, late);
+}
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
+    kv4_window_kernel(const __grid_constant__ AttnParams p) {
+    using W = Win<D, SPLIT>;
+    constexpr int kStages = W::kStages;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+    unsigned char* sm = smem_raw + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float* mul_s = reinterpret_cast<float*>(sm + W::kOffMul);
+    uint32_t* bad_s = reinterpret_cast<uint32_t*>(sm + W::kOffBad);
+    WinCursor* cur_s = reinterpret_cast<WinCursor*>(sm + W::kOffBar + W::kBars * 8);
+    uint32_t* tmem_s = reinterpret_cast<uint32_t*>(cur_s + 1);
+    const uint32_t bars = base + W::kOffBar;
+    const uint32_t k_full = bars, v_full = bars + 16;      // per stage: unpacked
+    const uint32_t s_done = bars + 32, p_ready = bars + 48, o_done = bars + 64;  // per parity of the tile
+    const uint32_t q_full = bars + 80, drained = bars + 88;
+    const int pairs = p.c.L * p.c.kv_heads;
+
+    if (warp == 8) {
+        const long long total = line_length(p, pairs, lane);
+        const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+        long long lo = 0, hi = 0;
+        WinCursor k{};
+        if (static_cast<int>(blockIdx.x) < ctas) {
+            cta_range(total, blockIdx.x, ctas, lo, hi);
+            k = find(p, pairs, lo, lane);
+        }
+        k.left = static_cast<int>(hi - lo);
+        if (lane == 0) *cur_s = k;
+    } else if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(k_full + 8 * i, kUnpackWarps);
+            mbar_init(v_full + 8 * i, kUnpackWarps);
+            mbar_init(s_done + 8 * i, 1);
+            mbar_init(p_ready + 8 * i, kSoftWarps);
+            mbar_init(o_done + 8 * i, 1);
+        }
+        mbar_init(q_full, kSoftWarps);
+        mbar_init(drained, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    WinCursor cur = *cur_s;
+    griddep_launch_dependents();
+    if (cur.left <= 0) return;
+    if (warp == 0) tmem_alloc(smem_addr(tmem_s), W::kTmCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_s;
+
+    // Tile n of the CTA (counted over all its units) uses stage n mod kStages of K and V and buffer n mod 2 of the scores.
+    auto stage_parity = [](int n) -> uint32_t { return static_cast<uint32_t>(n / kStages) & 1u; };
+    auto tile_parity = [](int n) -> uint32_t { return static_cast<uint32_t>(n >> 1) & 1u; };
+    bool failed = false;
+    int n = 0;
+
+    if (warp < kSoftWarps) {
+        // ------------------------------------------------------------------ rows
+        const int row = 32 * warp + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+        for (; cur.left > 0 && !failed; next_unit(p, pairs, cur)) {
+            int r0, r1;
+            unit_tiles(cur, r0, r1);
+            if (r1 <= r0) break;
+            const Unit x = win_unit(p, cur);
+            const int b = cur.b;
+            const int rows = static_cast<int>(min(static_cast<long long>(x.n) * p.group - x.col0, static_cast<long long>(kRows)));
+            if (tid == 0 && x.n > kv4_window(p.c, b).cap - x.start) atomicOr(&g_kv4_window_error, kErrBadPage);
+            // queries of this warp's rows, scaled to fill fp16's range
+#pragma unroll 2
+            for (int i = 0; i < 32; ++i) {
+                const int rr = 32 * warp + i;
+                if (rr >= rows) break;
+                constexpr int kChunks = D > 128 ? D / 128 : 1;
+                float4 v[kChunks];
+                float a = 0.0f;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    v[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (4 * lane + 128 * c < D) v[c] = load_q4(p, q_row(p, b, x, x.col0 + rr) + 128 * c + 4 * lane);
+                    a = fmaxf(fmaxf(a, fmaxf(fabsf(v[c].x), fabsf(v[c].y))), fmaxf(fabsf(v[c].z), fabsf(v[c].w)));
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
+                const float f = row_factor(a);
+                if (lane == 0) mul_s[rr] = fmaxf(p.scale_log2 / f, kLeastScale);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const int d = 4 * lane + 128 * c;
+                    if (d >= D) continue;
+                    const uint32_t at = (d >> 6) * W::kQBlock + sw128_offset(rr, (d & 63) >> 3) + (d & 7) * 2;
+                    const float q0 = v[c].x * f, q1 = v[c].y * f, q2 = v[c].z * f, q3 = v[c].w * f;
+                    const uint2 hi = make_uint2(pack_half2(q0, q1), pack_half2(q2, q3));
+                    *reinterpret_cast<uint2*>(sm + at) = hi;
+                    if constexpr (SPLIT)
+                        *reinterpret_cast<uint2*>(sm + W::kQBytes + at) =
+                            make_uint2(pack_rest(q0, q1, hi.x), pack_rest(q2, q3, hi.y));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_local(q_full);
+
+            const bool some = 32 * warp < rows;  // this warp has rows
+            const float mul = row < rows ? mul_s[row] : kLeastScale;
+            const int lim = row < rows ? min(x.start + (x.col0 + row) / p.group, x.end - 1) : -1;
+            const int seen_by_all = min(x.start + x.col0 / p.group + 1, x.end);
+            float m = -INFINITY, shift = kNone, l = 0.0f;
+            for (int r = r0; r < r1; ++r, ++n) {
+                if (!warp_wait(s_done + 8 * (n & 1), tile_parity(n))) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after();
+                if (some) {
+                    const uint32_t s_at = lanes + 64 * (n & 1);
+                    const int p0 = r * kTok;
+                    const uint32_t bad = bad_s[n & 3];
+                    const bool part = p0 + kTok > seen_by_all || bad != 0;
+                    // scores 32 h .. 32 h + 31 of the row, masked
+                    auto scores = [&](int h, float (&s)[32]) {
+                        tmem_read32(s_at + 32 * h, s);
+                        if (part) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (p0 + 32 * h + i > lim || ((bad >> (2 * h + (i >> 4))) & 1u)) s[i] = -INFINITY;
+                        }
+                    };
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // read twice rather than kept: 64 registers
+                        float s[32];
+                        scores(h, s);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i]);
+                    }
+                    if (__any_sync(~0u, fmaf(top, mul, shift) > kPShift + kSlack)) {
+                        const float v = fmaxf(m, top * mul);
+                        const float al = v == m ? 1.0f : exp2_approx(m - v);
+                        m = v;
+                        shift = v == -INFINITY ? kNone : kPShift - v;
+                        l *= al;
+                        if (r > r0) {  // the sums so far: after the product that is adding to them
+                            if (!warp_wait(o_done + 8 * ((n - 1) & 1), tile_parity(n - 1))) {
+                                failed = true;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                float o[32];
+                                uint32_t w[32];
+                                tmem_read32(lanes + W::kTmO + c, o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * al);
+                                tmem_st32(lanes + W::kTmO + c, w);
+                            }
+                        }
+                    }
+                    uint32_t lo[SPLIT ? 16 : 1];
+                    float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float s[32];
+                        uint32_t hi[16];
+                        scores(h, s);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float e0 = exp2_approx(fmaf(s[2 * i], mul, shift));
+                            const float e1 = exp2_approx(fmaf(s[2 * i + 1], mul, shift));
+                            sum0 += e0;
+                            sum1 += e1;
+                            hi[i] = pack_half2(e0, e1);
+                            s[2 * i] = e0;
+                            s[2 * i + 1] = e1;
+                        }
+                        tmem_st16(s_at + 16 * h, hi);
+                        if constexpr (SPLIT) {  // the first half's rests would overwrite scores not yet read
+                            uint32_t rest[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) rest[i] = pack_rest(s[2 * i], s[2 * i + 1], hi[i]);
+                            if (h == 1) {
+                                tmem_st16(s_at + 32, lo);
+                                tmem_st16(s_at + 48, rest);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) lo[i] = rest[i];
+                            }
+                        }
+                    }
+                    l += sum0 + sum1;
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_local(p_ready + 8 * (n & 1));
+            }
+            if (failed) break;
+            // outputs
+            if (!warp_wait(o_done + 8 * ((n - 1) & 1), tile_parity(n - 1))) {
+                failed = true;
+                break;
+            }
+            tc_fence_after();
+            if (some) {
+                const bool done = r0 == 0 && r1 == cur.cost - kStartCost;
+                float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kRows * (D + 2));
+                const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // no key at all: zeros
+                const size_t out = row < rows ? q_row(p, b, x, x.col0 + row) : 0;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    __syncwarp();
+                    tmem_read32(lanes + W::kTmO + c, o);
+                    if (row < rows && done) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) store_out2(p, out + c + i, o[i] * inv, o[i + 1] * inv);
+                    } else if (row < rows) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4*>(slot + row * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                }
+                if (!done && row < rows) {
+                    slot[kRows * D + row] = m;
+                    slot[kRows * D + kRows + row] = l;
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+        }
+    } else if (warp < kSoftWarps + kUnpackWarps) {
+        // ---------------------------------------------------------------- unpack
+        constexpr int kChunksPerRow = D / 32;            // 16 bytes of codes: 32 dims, two scales
+        constexpr int kMine = D / 64;                    // chunks of K (and of V) per thread
+        const int uw = warp - kSoftWarps;
+        const int psize = 1 << p.c.page_shift;
+        const int shift = min(p.c.page_shift, 6);
+        const uint32_t head_bytes = static_cast<uint32_t>(kv4_head_bytes(psize, D)), page_bytes = head_bytes * p.c.kv_heads;
+        int row[kMine], lc[kMine];
+        uint32_t dst[kMine], code_at[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int c = 16 * i + 4 * uw + (lane >> 3);
+            row[i] = (c / kChunksPerRow) * 8 + (lane & 7);
+            const int pc = c % kChunksPerRow;
+            lc[i] = pc ^ (kv4_swizzle(row[i], D / 16) >> 1);
+            code_at[i] = pc * 16;
+            dst[i] = (lc[i] >> 1) * W::kKvBlock;
+        }
+        WinCursor ahead = cur;   // of the tile whose data is requested next
+        int a_r = 0, a_r1 = 0;
+        Unit a{};
+        bool more = true;
+        // steps to the next tile; false at the end of the CTA's places
+        auto step = [&]() {
+            if (++a_r < a_r1) return;
+            for (;;) {
+                if (ahead.left <= 0) {
+                    more = false;
+                    return;
+                }
+                int r0, r1;
+                unit_tiles(ahead, r0, r1);
+                a = win_unit(p, ahead);
+                a_r = r0;
+                a_r1 = r1;
+                const int b = ahead.b;
+                next_unit(p, pairs, ahead);
+                a.n = b;  // (the sequence; its token count is not needed here)
+                if (r1 > r0) return;
+            }
+        };
+        a_r1 = -1;
+        step();
+        uint4 kc[kMine], vc[kMine];
+        uint32_t ks[kMine], vs[kMine];
+        uint32_t bad = 0;
+        auto fetch = [&]() {
+            const int p0 = a_r * kTok;
+            // lane j < 4 looks up page j of the tile (one page, or several of a tile)
+            const int pos = p0 + (lane << shift);
+            const bool want = lane < (kTok >> shift) && pos < a.end;
+            const int page = want ? kv4_page(p.c, a.n, pos) : -2;
+            const unsigned gone = __ballot_sync(~0u, page == -1);
+            // the missing pages as 16-token groups, whatever the page size
+            bad = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) bad |= ((gone >> ((16 * q) >> shift)) & 1u) << q;
+            const uint8_t* head = p.c.cache + (static_cast<size_t>(a.l) * p.c.n_pages * p.c.kv_heads + a.h) * head_bytes;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int j = row[i] >> shift;
+                const int pg = __shfl_sync(~0u, page, j);
+                kc[i] = vc[i] = make_uint4(0u, 0u, 0u, 0u);
+                ks[i] = vs[i] = 0u;
+                if (pg >= 0 && p0 + row[i] < a.end) {
+                    const int in_page = (p0 & (psize - 1)) + row[i] - (j << shift);
+                    const uint8_t* k = head + static_cast<unsigned long long>(static_cast<uint32_t>(pg)) * page_bytes;
+                    const uint8_t* v = k + head_bytes / 2;
+                    kc[i] = __ldg(reinterpret_cast<const uint4*>(k + in_page * (D / 2) + code_at[i]));
+                    vc[i] = __ldg(reinterpret_cast<const uint4*>(v + in_page * (D / 2) + code_at[i]));
+                    const int sc = psize * (D / 2) + in_page * (D / 16) + 2 * lc[i];
+                    ks[i] = __ldg(reinterpret_cast<const uint16_t*>(k + sc));
+                    vs[i] = __ldg(reinterpret_cast<const uint16_t*>(v + sc));
+                }
+            }
+        };
+        // one chunk of 32 values, as fp16 in its swizzled row
+        auto put = [&](unsigned char* tile, const uint4& code, uint32_t scales, int i) {
+            const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t v[4];
+                unpack(w[j], scale_twice(scales, j >> 1), v);
+                *reinterpret_cast<uint4*>(tile + dst[i] + sw128_offset(row[i], (lc[i] & 1) * 4 + j)) =
+                    make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        };
+        if (more) fetch();
+        while (more) {
+            const int s = n % kStages;
+            if (n >= kStages && !warp_wait(s_done + 8 * ((n - kStages) & 1), tile_parity(n - kStages))) {
+                failed = true;
+                break;
+            }
+            unsigned char* kt = sm + W::kOffK + s * W::kKvBytes;
+            unsigned char* vt = sm + W::kOffV + s * W::kKvBytes;
+            if (warp == kSoftWarps && lane == 0) {
+                bad_s[n & 3] = bad;
+                if (bad != 0) atomicOr(&g_kv4_window_error, kErrBadPage);
+            }
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) put(kt, kc[i], ks[i], i);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_local(k_full + 8 * s);
+            if (n >= kStages && !warp_wait(o_done + 8 * ((n - kStages) & 1), tile_parity(n - kStages))) {
+                failed = true;
+                break;
+            }
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) put(vt, vc[i], vs[i], i);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_local(v_full + 8 * s);
+            ++n;
+            step();
+            if (more) fetch();
+        }
+    } else if (lane == 0) {
+        // -------------------------------------------------------------- products
+        const uint32_t idesc_s = idesc_f16(kTok), idesc_o = idesc_f16(D) | kIdescBMnMajor;
+        int units = 0;
+        // O += P V of tile t
+        auto second = [&](int t, bool first) -> bool {
+            const int s = t % kStages;
+            if (!mbar_wait_bounded(v_full + 8 * s, stage_parity(t))) return false;
+            if (!mbar_wait_bounded(p_ready + 8 * (t & 1), tile_parity(t))) return false;
+            tc_fence_after();
+            const uint32_t v = base + W::kOffV + s * W::kKvBytes;
+#pragma unroll
+            for (int kk = 0; kk < kTok / 16; ++kk) {
+                mma_f16_ta(tmem + W::kTmO, tmem + 64 * (t & 1) + 8 * kk, sw128_mn_desc(v + kk * 2048, W::kKvBlock), idesc_o,
+                           first && kk == 0 ? 0u : 1u);
+                if constexpr (SPLIT)
+                    mma_f16_ta(tmem + W::kTmO, tmem + 64 * (t & 1) + 32 + 8 * kk, sw128_mn_desc(v + kk * 2048, W::kKvBlock),
+                               idesc_o, 1u);
+            }
+            mma_commit(o_done + 8 * (t & 1));
+            return true;
+        };
+        for (; cur.left > 0 && !failed; next_unit(p, pairs, cur)) {
+            int r0, r1;
+            unit_tiles(cur, r0, r1);
+            if (r1 <= r0) break;
+            if (!mbar_wait_bounded(q_full, static_cast<uint32_t>(units) & 1u)) {
+                failed = true;
+                break;
+            }
+            ++units;
+            for (int r = r0; r < r1 && !failed; ++r, ++n) {
+                const int s = n % kStages;
+                // (the buffer's last reader, the second product of tile n - 2, has completed)
+                if (!mbar_wait_bounded(k_full + 8 * s, stage_parity(n)) ||
+                    (n >= 2 && !mbar_wait_bounded(o_done + 8 * (n & 1), tile_parity(n - 2)))) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t k = base + W::kOffK + s * W::kKvBytes;
+#pragma unroll
+                for (int blk = 0; blk < W::kBlk; ++blk)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t kd = sw128_desc(k + blk * W::kKvBlock) + 2 * kk;
+                        mma_bf16(tmem + 64 * (n & 1), sw128_desc(base + blk * W::kQBlock) + 2 * kk, kd, idesc_s,
+                                 (blk | kk) == 0 ? 0u : 1u);
+                        if constexpr (SPLIT)
+                            mma_bf16(tmem + 64 * (n & 1), sw128_desc(base + W::kQBytes + blk * W::kQBlock) + 2 * kk, kd, idesc_s, 1u);
+                    }
+                mma_commit(s_done + 8 * (n & 1));
+                if (r > r0 && !second(n - 1, r - 1 == r0)) failed = true;
+            }
+            if (!failed && !second(n - 1, r1 - 1 == r0)) failed = true;
+        }
+        // whatever was issued has completed before the tensor memory is freed
+        mma_commit(drained);
+        (void)mbar_wait_bounded(drained, 0);
+    }
+    if (failed && lane == 0) atomicOr(&g_kv4_window_error, kErrWaitTimeout);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, W::kTmCols);
+    }
+}
+
+// Joins the partial results of the units that several CTAs shared: a block per CTA that such a unit starts in and
+// group of four rows, a warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) kv4_window_join_kernel(const __grid_constant__ AttnParams p) {
+    constexpr size_t kSlot = kRows * (D + 2);
+    const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const int pairs = p.c.L * p.c.kv_heads;
+    const long long total = line_length(p, pairs, lane);
+    const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+    long long lo = 0, hi = 0, first = 0, end = 0;
+    WinCursor k{};
+    bool mine = false;
+    if (static_cast<int>(blockIdx.x) < n) {
+        cta_range(total, blockIdx.x, n, lo, hi);
+        k = find(p, pairs, hi - 1, lane);
+        first = hi - 1 - k.at;
+        end = first + k.cost;
+        mine = first + kStartCost >= lo && k.at >= kStartCost && end > hi;
+    }
+    griddep_wait();  // in every block: the grid must not end before the one it follows
+    if (!mine) return;
+    const Unit x = win_unit(p, k);
+    if (row >= static_cast<long long>(x.n) * p.group - x.col0) return;
+    const int parts = cta_of(total, end - 1, n) - static_cast<int>(blockIdx.x) + 1;
+    const float* base = p.part + static_cast<size_t>(blockIdx.x) * 2 * kSlot;
+    auto slot = [&](int i) -> const float* { return i == 0 ? base + kSlot : base + static_cast<size_t>(i) * 2 * kSlot; };
+    float mm = -INFINITY;
+    for (int i = 0; i < parts; ++i) mm = fmaxf(mm, slot(i)[kRows * D + row]);
+    float2 v[D / 64];
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) v[c] = make_float2(0.0f, 0.0f);
+    float l = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+        const float* s = slot(i);
+        const float ms = s[kRows * D + row];
+        const float f = ms == -INFINITY ? 0.0f : exp2_approx(ms - mm);
+        l += s[kRows * D + kRows + row] * f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const float2 y = *reinterpret_cast<const float2*>(s + row * D + 64 * c + 2 * lane);
+            v[c].x += y.x * f;
+            v[c].y += y.y * f;
+        }
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    const size_t out = q_row(p, k.b, x, x.col0 + row) + 2 * lane;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) store_out2(p, out + 64 * c, v[c].x * inv, v[c].y * inv);
+}
+
+constexpr int kMaxSms = 192;  // the workspace is sized for cards of up to as many
+
+template <int D, bool SPLIT>
+cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
+    using W = Win<D, SPLIT>;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
+    if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1u)) {
+        e = cudaFuncSetAttribute(kv4_window_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+    }
+    static_assert(W::kCtas * (W::kSmem + 1024) <= 233472, "the CTAs of an SM fit its shared memory");
+    const int ctas = W::kCtas * std::min(sms, kMaxSms);
+    kv4_window_kernel<D, SPLIT><<<ctas, kWinThreads, W::kSmem, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const long long rows = std::min<long long>(static_cast<long long>(p.c.T) * p.group, kRows);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, static_cast<unsigned>((rows + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_window_join_kernel<D>, p);
+}
+
+template <int D>
+cudaError_t launch_dim(const AttnParams& p, cudaStream_t stream) {
+    return p.dtype == DType::kF32 ? launch_one<D, true>(p, stream) : launch_one<D, false>(p, stream);
+}
+
+}  // namespace
+
+size_t kv4_window_workspace_bytes(int head_dim) {
+    return static_cast<size_t>(2 * kMaxSms) * 2 * kRows * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_kv4_window(AttnParams p, cudaStream_t stream) {
+    p.col_blocks = static_cast<int>((static_cast<long long>(p.c.T) * p.group + kRows - 1) / kRows);
+    switch (p.c.head_dim) {
+        case 64: return launch_dim<64>(p, stream);
+        case 128: return launch_dim<128>(p, stream);
+        case 256: return launch_dim<256>(p, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t read_kv4_window_error(uint32_t* out) {
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv4_window_error, sizeof(v));
+    if (e != cudaSuccess) return e;
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_kv4_window_error, &zero, sizeof(zero));
+    *out = v;
+    return e;
+}
+
+}  // namespace gdn

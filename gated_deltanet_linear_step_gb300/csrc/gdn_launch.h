@@ -150,7 +150,8 @@ cudaError_t launch_decode_window_tc(const StepArgs& a, cudaStream_t stream);
 cudaError_t read_window_tc_error(uint32_t* out);
 
 // Reads and clears the device error words of the 4-bit cache's and its attention's kernels
-// (gdn_kv4_cache.cu, gdn_kv4_attention.cu).
+// (gdn_kv4_cache.cu, gdn_kv4_attention.cu, gdn_kv4_window.cu).
+cudaError_t read_kv4_window_error(uint32_t* out);
 cudaError_t read_kv4_cache_error(uint32_t* out);
 cudaError_t read_kv4_attention_error(uint32_t* out);
 

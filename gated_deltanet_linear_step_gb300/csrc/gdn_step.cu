@@ -730,11 +730,13 @@ cudaError_t read_device_error(cudaStream_t stream, uint32_t* out) {
     uint32_t v5 = 0;
     e = read_window_tc_error(&v5);
     if (e != cudaSuccess) return e;
-    uint32_t v6 = 0, v7 = 0;
+    uint32_t v6 = 0, v7 = 0, v8 = 0;
+    e = read_kv4_window_error(&v8);
+    if (e != cudaSuccess) return e;
     e = read_kv4_cache_error(&v6);
     if (e != cudaSuccess) return e;
     e = read_kv4_attention_error(&v7);
-    *out = v | v1 | v2 | v3 | v4 | v5 | v6 | v7;
+    *out = v | v1 | v2 | v3 | v4 | v5 | v6 | v7 | v8;
     return e;
 }
 
