@@ -250,6 +250,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
     const int units = p.c.L * p.c.kv_heads * p.col_blocks;
     const long long total = all_costs<D>(p.c, lane) * units;
     const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+    JoinRecord* record = reinterpret_cast<JoinRecord*>(p.records) + blockIdx.x;
+    if (tid == 0) *record = JoinRecord{0, 0, 0, 0};
     if (static_cast<int>(blockIdx.x) >= ctas) return;
     long long lo, hi;
     cta_range(total, blockIdx.x, ctas, lo, hi);
@@ -718,6 +720,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
             __syncthreads();
         }
         if (owed) issue();
+        if (tid == 0 && !done && r0 == 0)  // this CTA's blocks of the join have it
+            *record = JoinRecord{cur.b, cur.u % p.col_blocks, cur.u / p.col_blocks,
+                                 cta_of(total, hi - cur.left - cur.at + cur.cost - 1, ctas) - static_cast<int>(blockIdx.x) + 1};
 
         // --- the next unit
         advance<D>(p.c, units, cur);
@@ -732,24 +737,12 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ A
     __shared__ float2 sums[128];
     __shared__ float lsum[128];
     const int lane = threadIdx.x & 31, c = blockIdx.y;
-    const int units = p.c.L * p.c.kv_heads * p.col_blocks;
-    const long long total = all_costs<D>(p.c, lane) * units;
-    const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-    long long lo = 0, hi = 0, first = 0, end = 0;
-    Cursor k{};
-    bool mine = false;  // the unit that this CTA's last place belongs to has rounds that start here and end elsewhere
-    if (static_cast<int>(blockIdx.x) < n) {
-        cta_range(total, blockIdx.x, n, lo, hi);
-        k = locate<D>(p.c, units, hi - 1, lane);
-        first = hi - 1 - k.at;
-        end = first + k.cost;
-        mine = first + kUnitCost >= lo && k.at >= kUnitCost && end > hi;
-    }
-    griddep_wait();  // in every block: the grid must not end before the one it follows
-    if (!mine) return;
-    const Unit x = unit_of(p, k.b, k.u, kCols);
+    griddep_wait();
+    const JoinRecord rec = reinterpret_cast<const JoinRecord*>(p.records)[blockIdx.x];
+    if (rec.parts == 0) return;
+    const Unit x = unit_of(p, rec.b, rec.pair * p.col_blocks + rec.block, kCols);
     if (c >= min(x.n * p.group - x.col0, kCols)) return;
-    const int parts = cta_of(total, end - 1, n) - static_cast<int>(blockIdx.x) + 1;
+    const int parts = rec.parts;
     const float* base = p.part + static_cast<size_t>(blockIdx.x) * 2 * kSlot;
     auto slot = [&](int i) -> const float* { return i == 0 ? base + kSlot : base + static_cast<size_t>(i) * 2 * kSlot; };
     float mm = -INFINITY;
@@ -778,7 +771,7 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ A
         l += lsum[w * kPairs + pair];
     }
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    store_out2(p, q_row(p, k.b, x, x.col0 + c) + dim_of<D>(2 * pair), v.x * inv, v.y * inv);
+    store_out2(p, q_row(p, rec.b, x, x.col0 + c) + dim_of<D>(2 * pair), v.x * inv, v.y * inv);
 }
 
 // Windows of more query rows per kv head than this go to the tensor cores (gdn_kv4_window.cu).
@@ -842,7 +835,7 @@ size_t kv4_attention_workspace_bytes(int B, int L, int T, int q_heads, int kv_he
     const int group = q_heads / kv_heads;
     if (on_tensor_cores(T, group)) return kv4_window_workspace_bytes(head_dim);
     const int nt = column_tiles(T, group);
-    return static_cast<size_t>(kMaxCtas) * 2 * (8 * nt) * (head_dim + 2) * sizeof(float);
+    return static_cast<size_t>(kMaxCtas) * (2 * (8 * nt) * (head_dim + 2) * sizeof(float) + sizeof(JoinRecord));
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t stream) {
@@ -858,6 +851,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t stream) {
     if (on_tensor_cores(a.c.T, p.group)) return launch_kv4_window(p, stream);
     const int nt = column_tiles(a.c.T, p.group);
     p.col_blocks = static_cast<int>((static_cast<long long>(a.c.T) * p.group + 8 * nt - 1) / (8 * nt));
+    p.records = p.part + static_cast<size_t>(kMaxCtas) * 2 * (8 * nt) * (a.c.head_dim + 2);
     switch (a.c.head_dim) {
         case 64: return launch_dim<64>(p, nt, stream);
         case 128: return launch_dim<128>(p, nt, stream);

@@ -11,11 +11,18 @@ constexpr float kPShift = 8.0f;  // probabilities are kept relative to 2^-8 of t
 constexpr float kSlack = 6.0f;   // ... which is raised when a score exceeds it by 6: none is above 2^14
 constexpr float kNone = 1e30f;   // the shift of a column that has seen no key
 
+// The unit, if there is one, whose first rounds a CTA did and whose last ones other CTAs did: what the joining kernel
+// needs to know. `parts` CTAs, this one first, have a partial result of it each.
+struct JoinRecord {
+    int b, block, pair, parts;  // pair: layer and kv head
+};
+
 struct AttnParams {
     Kv4Cache c;
     const void* q;
     void* out;
-    float* part;  // per CTA two partial results: [columns][D] sums, then maxima and sums of the columns
+    float* part;    // per CTA two partial results: [columns][D] sums, then maxima and sums of the columns
+    void* records;  // per CTA a JoinRecord
     int q_heads, group, col_blocks;
     DType dtype;
     float scale_log2;

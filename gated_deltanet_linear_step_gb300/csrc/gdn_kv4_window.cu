@@ -11,13 +11,14 @@
 // pipe, and unpacking and softmax about 500 issue slots of each of its four schedulers; the roles below
 // overlap the three, and two CTAs per SM (D <= 128) fill each other's waits.
 //
-//   warps 0-3  a row per thread: queries in, the softmax of a tile from tensor
+//   warps 0-7  half a row per thread (warps w and w + 4 share rows and exchange their
+//              halves' maxima): queries in, the softmax of a tile from tensor
 //              memory, probabilities back to tensor memory (fp16, over the scores they
 //              came from, as the A operand of the second product), outputs out
-//   warps 4-7  unpack the next tiles: 16 bytes of codes per thread from global
+//   warps 8-11 unpack the next tiles: 16 bytes of codes per thread from global
 //              memory, a tile ahead in registers, to fp16 in the swizzled
 //              K-major rows that both products read (V with its rows as K: MN-major)
-//   warp 8     issues the products
+//   warp 12    issues the products
 //
 // Scores have two buffers in tensor memory, K and V tiles two stages each, so
 // the product of tile j + 1 runs during the softmax of tile j. The
@@ -45,7 +46,8 @@ namespace {
 
 constexpr int kRows = 128;       // of a block
 constexpr int kTok = 64;         // of a tile
-constexpr int kSoftWarps = 4, kUnpackWarps = 4;
+constexpr int kSoftWarps = 8, kUnpackWarps = 4;
+constexpr int kIssueWarp = kSoftWarps + kUnpackWarps;
 constexpr int kWinThreads = 32 * (kSoftWarps + kUnpackWarps + 1);
 constexpr int kStartCost = 4;    // places of a block's start on the line, in tiles
 
@@ -63,8 +65,9 @@ struct Win {
     static constexpr uint32_t kOffV = kOffK + kStages * kKvBytes;
     static constexpr uint32_t kOffMul = kOffV + kStages * kKvBytes;  // factor of a row's raw scores
     static constexpr uint32_t kOffBad = kOffMul + kRows * 4;         // missing pages of tiles j mod 4
-    static constexpr uint32_t kOffBar = kOffBad + 4 * 4;
-    static constexpr uint32_t kBars = 2 + 2 + 2 + 2 + 2 + 1 + 1;     // see below
+    static constexpr uint32_t kOffXch = kOffBad + 4 * 4;             // what the two halves of a row tell each other
+    static constexpr uint32_t kOffBar = kOffXch + 2 * 2 * kRows * 4;
+    static constexpr uint32_t kBars = 2 + 2 + 2 + 2 + 2 + 1 + 1 + 4;  // see below
     static constexpr uint32_t kUsed = kOffBar + kBars * 8 + 64;      // + cursor, tensor memory address
     static constexpr int kCtas = D <= 128 && 2 * (kUsed + 2048) <= 232448 ? 2 : 1;
     // no more CTAs than the tensor memory has room for: a third (second) would wait in its allocation
@@ -93,66 +96,44 @@ __device__ __forceinline__ int block_cost(const AttnParams& p, const Kv4Window& 
     return end == 0 ? 0 : kStartCost + (end + kTok - 1) / kTok;
 }
 
-// Places of sequence b, of one (layer, kv head) pair.
-__device__ __forceinline__ int seq_cost(const AttnParams& p, int b) {
-    const Kv4Window w = kv4_window(p.c, b);
-    int s = 0;
-    for (int blk = 0; blk < p.col_blocks; ++blk) {
-        const int c = block_cost(p, w, blk);
-        if (c == 0) break;
-        s += c;
-    }
-    return s;
+// Cost of block i % col_blocks of sequence i / col_blocks.
+__device__ __forceinline__ int item_cost(const AttnParams& p, int i) {
+    const int b = i / p.col_blocks;
+    return block_cost(p, kv4_window(p.c, b), i - b * p.col_blocks);
 }
 
 __device__ __forceinline__ long long line_length(const AttnParams& p, int pairs, int lane) {
     long long s = 0;
-    for (int b = lane; b < p.c.B; b += 32) s += seq_cost(p, b);
+    for (int i = lane; i < p.c.B * p.col_blocks; i += 32) s += item_cost(p, i);
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
     return s * pairs;
-}
-
-// Inclusive sums over the lanes.
-__device__ __forceinline__ long long scan(long long v, int lane) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(~0u, v, o);
-        if (lane >= o) v += y;
-    }
-    return v;
 }
 
 // The unit and place in it of place x of the line, by one warp.
 __device__ __forceinline__ WinCursor find(const AttnParams& p, int pairs, long long x, int lane) {
     WinCursor k{p.c.B, 0, 0, 0, 0, 0};
-    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-        const long long mine = b0 + lane < p.c.B ? static_cast<long long>(seq_cost(p, b0 + lane)) * pairs : 0;
-        const long long sum = scan(mine, lane);
+    const int items = p.c.B * p.col_blocks;
+    for (int i0 = 0; i0 < items; i0 += 32) {
+        const int cost = i0 + lane < items ? item_cost(p, i0 + lane) : 0;
+        long long sum = static_cast<long long>(cost) * pairs;
+        const long long mine = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += y;
+        }
         const unsigned hit = __ballot_sync(~0u, sum > x);
         if (hit == 0) {
             x -= __shfl_sync(~0u, sum, 31);
             continue;
         }
         const int src = __ffs(hit) - 1;
-        k.b = b0 + src;
+        k.b = (i0 + src) / p.col_blocks;
+        k.blk = i0 + src - k.b * p.col_blocks;
+        k.cost = __shfl_sync(~0u, cost, src);
         x -= __shfl_sync(~0u, sum - mine, src);
-        const Kv4Window w = kv4_window(p.c, k.b);
-        for (int m0 = 0; m0 < p.col_blocks; m0 += 32) {
-            const int cost = m0 + lane < p.col_blocks ? block_cost(p, w, m0 + lane) : 0;
-            const long long of_block = scan(static_cast<long long>(cost) * pairs, lane);
-            const unsigned at = __ballot_sync(~0u, of_block > x);
-            if (at == 0) {
-                x -= __shfl_sync(~0u, of_block, 31);
-                continue;
-            }
-            const int bl = __ffs(at) - 1;
-            k.blk = m0 + bl;
-            k.cost = __shfl_sync(~0u, cost, bl);
-            x -= __shfl_sync(~0u, of_block, bl) - static_cast<long long>(k.cost) * pairs;
-            k.lh = static_cast<int>(mul_div(x, 1, k.cost));
-            k.at = static_cast<int>(x - static_cast<long long>(k.lh) * k.cost);
-            return k;
-        }
+        k.lh = static_cast<int>(mul_div(x, 1, k.cost));
+        k.at = static_cast<int>(x - static_cast<long long>(k.lh) * k.cost);
         return k;
     }
     return k;
@@ -222,6 +203,42 @@ __device__ __forceinline__ void tmem_read32(uint32_t taddr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
 }
 
+// 16 consecutive columns of this warp's lanes, one lane per thread, complete when it returns.
+__device__ __forceinline__ void tmem_read16(uint32_t taddr, uint32_t (&u)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// 16 outputs of a row, times a factor.
+__device__ __forceinline__ void store_out16(const AttnParams& p, size_t i, const float (&o)[16], float f) {
+    if (p.dtype == DType::kF32) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + i + j) =
+                make_float4(o[j] * f, o[j + 1] * f, o[j + 2] * f, o[j + 3] * f);
+        return;
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (p.dtype == DType::kF16) {
+            w[j] = pack_half2(o[2 * j] * f, o[2 * j + 1] * f);
+        } else {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * j] * f, o[2 * j + 1] * f);
+            w[j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+    }
+    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + i);
+    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
 // Stores 16 consecutive columns of this warp's lanes, one lane per thread.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
@@ -254,12 +271,17 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
     const uint32_t bars = base + W::kOffBar;
     const uint32_t k_full = bars, v_full = bars + 16;      // per stage: unpacked
     const uint32_t s_done = bars + 32, p_ready = bars + 48, o_done = bars + 64;  // per parity of the tile
-    const uint32_t q_full = bars + 80, drained = bars + 88;
+    const uint32_t q_full = bars + 80, drained = bars + 88, pair = bars + 96;  // pair: per 32 rows
+    float* xch = reinterpret_cast<float*>(sm + W::kOffXch);
     const int pairs = p.c.L * p.c.kv_heads;
 
-    if (warp == 8) {
-        const long long total = line_length(p, pairs, lane);
-        const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+    long long total = 0;
+    int ctas = 0;
+    if (warp == 0 || warp == kIssueWarp) {
+        total = line_length(p, pairs, lane);
+        ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+    }
+    if (warp == kIssueWarp) {
         long long lo = 0, hi = 0;
         WinCursor k{};
         if (static_cast<int>(blockIdx.x) < ctas) {
@@ -278,11 +300,14 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
         }
         mbar_init(q_full, kSoftWarps);
         mbar_init(drained, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(pair + 8 * i, 2);
         fence_mbar_init();
     }
     __syncthreads();
     WinCursor cur = *cur_s;
     griddep_launch_dependents();
+    JoinRecord* record = reinterpret_cast<JoinRecord*>(p.records) + blockIdx.x;
+    if (tid == 0) *record = JoinRecord{0, 0, 0, 0};
     if (cur.left <= 0) return;
     if (warp == 0) tmem_alloc(smem_addr(tmem_s), W::kTmCols);
     tc_fence_before();
@@ -298,8 +323,24 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
 
     if (warp < kSoftWarps) {
         // ------------------------------------------------------------------ rows
-        const int row = 32 * warp + lane;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+        const int quarter = warp & 3, half = warp >> 2;
+        const int row = 32 * quarter + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+        const uint32_t my_pair = pair + 8 * quarter;
+        uint32_t met = 0;  // times the two halves have met
+        // This half's value of the row to the other half, and the other's value here.
+        auto exchange = [&](float v, float& other) -> bool {
+            float* x = xch + (met & 1) * 2 * kRows + row;
+            x[half * kRows] = v;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_local(my_pair);
+            if (!warp_wait(my_pair, met & 1)) return false;
+            tc_fence_after();
+            ++met;
+            other = x[(half ^ 1) * kRows];
+            return true;
+        };
         for (; cur.left > 0 && !failed; next_unit(p, pairs, cur)) {
             int r0, r1;
             unit_tiles(cur, r0, r1);
@@ -308,10 +349,10 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             const int b = cur.b;
             const int rows = static_cast<int>(min(static_cast<long long>(x.n) * p.group - x.col0, static_cast<long long>(kRows)));
             if (tid == 0 && x.n > kv4_window(p.c, b).cap - x.start) atomicOr(&g_kv4_window_error, kErrBadPage);
-            // queries of this warp's rows, scaled to fill fp16's range
+            // queries of half of these rows, scaled to fill fp16's range
 #pragma unroll 2
-            for (int i = 0; i < 32; ++i) {
-                const int rr = 32 * warp + i;
+            for (int i = 0; i < 16; ++i) {
+                const int rr = 32 * quarter + 16 * half + i;
                 if (rr >= rows) break;
                 constexpr int kChunks = D > 128 ? D / 128 : 1;
                 float4 v[kChunks];
@@ -342,8 +383,13 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_local(q_full);
+            float other;
+            if (!exchange(0.0f, other)) {  // the other half's rows have their factors
+                failed = true;
+                break;
+            }
 
-            const bool some = 32 * warp < rows;  // this warp has rows
+            const bool some = 32 * quarter < rows;  // this warp has rows
             const float mul = row < rows ? mul_s[row] : kLeastScale;
             const int lim = row < rows ? min(x.start + (x.col0 + row) / p.group, x.end - 1) : -1;
             const int seen_by_all = min(x.start + x.col0 / p.group + 1, x.end);
@@ -356,81 +402,63 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                 tc_fence_after();
                 if (some) {
                     const uint32_t s_at = lanes + 64 * (n & 1);
-                    const int p0 = r * kTok;
-                    const uint32_t bad = bad_s[n & 3];
-                    const bool part = p0 + kTok > seen_by_all || bad != 0;
-                    // scores 32 h .. 32 h + 31 of the row, masked
-                    auto scores = [&](int h, float (&s)[32]) {
-                        tmem_read32(s_at + 32 * h, s);
-                        if (part) {
+                    const int p0 = r * kTok + 32 * half;  // this half's first position
+                    const uint32_t bad = bad_s[n & 3] >> (2 * half);
+                    float s[32];
+                    tmem_read32(s_at + 32 * half, s);
+                    if (p0 + 32 > seen_by_all || bad != 0) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (p0 + 32 * h + i > lim || ((bad >> (2 * h + (i >> 4))) & 1u)) s[i] = -INFINITY;
-                        }
-                    };
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // read twice rather than kept: 64 registers
-                        float s[32];
-                        scores(h, s);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i]);
+                        for (int i = 0; i < 32; ++i)
+                            if (p0 + i > lim || ((bad >> (i >> 4)) & 1u)) s[i] = -INFINITY;
                     }
+                    float t[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int i = 4; i < 32; ++i) t[i & 3] = fmaxf(t[i & 3], s[i]);
+                    float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                    if (!exchange(top, other)) {  // after it both halves have read their scores
+                        failed = true;
+                        break;
+                    }
+                    top = fmaxf(top, other);
                     if (__any_sync(~0u, fmaf(top, mul, shift) > kPShift + kSlack)) {
                         const float v = fmaxf(m, top * mul);
                         const float al = v == m ? 1.0f : exp2_approx(m - v);
                         m = v;
                         shift = v == -INFINITY ? kNone : kPShift - v;
                         l *= al;
-                        if (r > r0) {  // the sums so far: after the product that is adding to them
+                        if (r > r0) {  // this half of the sums so far: after the product that is adding to them
                             if (!warp_wait(o_done + 8 * ((n - 1) & 1), tile_parity(n - 1))) {
                                 failed = true;
                                 break;
                             }
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                float o[32];
-                                uint32_t w[32];
-                                tmem_read32(lanes + W::kTmO + c, o);
+                            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                                uint32_t w[16];
+                                tmem_read16(lanes + W::kTmO + c, w);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * al);
-                                tmem_st32(lanes + W::kTmO + c, w);
+                                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * al);
+                                tmem_st16(lanes + W::kTmO + c, w);
                             }
                         }
                     }
-                    uint32_t lo[SPLIT ? 16 : 1];
-                    float sum0 = 0.0f, sum1 = 0.0f;
+                    float sum[2] = {0.0f, 0.0f};
+                    uint32_t hi[16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float s[32];
-                        uint32_t hi[16];
-                        scores(h, s);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float e0 = exp2_approx(fmaf(s[2 * i], mul, shift));
-                            const float e1 = exp2_approx(fmaf(s[2 * i + 1], mul, shift));
-                            sum0 += e0;
-                            sum1 += e1;
-                            hi[i] = pack_half2(e0, e1);
-                            s[2 * i] = e0;
-                            s[2 * i + 1] = e1;
-                        }
-                        tmem_st16(s_at + 16 * h, hi);
-                        if constexpr (SPLIT) {  // the first half's rests would overwrite scores not yet read
-                            uint32_t rest[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) rest[i] = pack_rest(s[2 * i], s[2 * i + 1], hi[i]);
-                            if (h == 1) {
-                                tmem_st16(s_at + 32, lo);
-                                tmem_st16(s_at + 48, rest);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) lo[i] = rest[i];
-                            }
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        s[2 * i] = exp2_approx(fmaf(s[2 * i], mul, shift));
+                        s[2 * i + 1] = exp2_approx(fmaf(s[2 * i + 1], mul, shift));
+                        sum[0] += s[2 * i];
+                        sum[1] += s[2 * i + 1];
+                        hi[i] = pack_half2(s[2 * i], s[2 * i + 1]);
                     }
-                    l += sum0 + sum1;
+                    l += sum[0] + sum[1];
+                    tmem_st16(s_at + 16 * half, hi);
+                    if constexpr (SPLIT) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) hi[i] = pack_rest(s[2 * i], s[2 * i + 1], hi[i]);
+                        tmem_st16(s_at + 32 + 16 * half, hi);
+                    }
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -438,37 +466,44 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                 if (lane == 0) mbar_arrive_local(p_ready + 8 * (n & 1));
             }
             if (failed) break;
-            // outputs
-            if (!warp_wait(o_done + 8 * ((n - 1) & 1), tile_parity(n - 1))) {
+            // outputs: each half its dims
+            if (!exchange(l, other) || !warp_wait(o_done + 8 * ((n - 1) & 1), tile_parity(n - 1))) {
                 failed = true;
                 break;
             }
+            l = half == 0 ? l + other : other + l;
             tc_fence_after();
+            const bool done = r0 == 0 && r1 == cur.cost - kStartCost;
             if (some) {
-                const bool done = r0 == 0 && r1 == cur.cost - kStartCost;
                 float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kRows * (D + 2));
                 const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // no key at all: zeros
                 const size_t out = row < rows ? q_row(p, b, x, x.col0 + row) : 0;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
+                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                    uint32_t w[16];
                     __syncwarp();
-                    tmem_read32(lanes + W::kTmO + c, o);
-                    if (row < rows && done) {
+                    tmem_read16(lanes + W::kTmO + c, w);
+                    float o[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) store_out2(p, out + c + i, o[i] * inv, o[i + 1] * inv);
+                    for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(w[i]);
+                    if (row < rows && done) {
+                        store_out16(p, out + c, o, inv);
                     } else if (row < rows) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
+                        for (int i = 0; i < 16; i += 4)
                             *reinterpret_cast<float4*>(slot + row * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     }
                 }
-                if (!done && row < rows) {
+                if (!done && half == 0 && row < rows) {
                     slot[kRows * D + row] = m;
                     slot[kRows * D + kRows + row] = l;
                 }
                 __syncwarp();
             }
+            if (tid == 0 && !done && r0 == 0)  // this CTA's block of the join has it
+                *record = JoinRecord{cur.b, cur.blk, cur.lh,
+                                     cta_of(total, mul_div(total, blockIdx.x + 1, ctas) - cur.at - cur.left + cur.cost - 1, ctas) -
+                                         static_cast<int>(blockIdx.x) + 1};
             tc_fence_before();
         }
     } else if (warp < kSoftWarps + kUnpackWarps) {
@@ -479,17 +514,15 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
         const int psize = 1 << p.c.page_shift;
         const int shift = min(p.c.page_shift, 6);
         const uint32_t head_bytes = static_cast<uint32_t>(kv4_head_bytes(psize, D)), page_bytes = head_bytes * p.c.kv_heads;
-        int row[kMine], lc[kMine];
-        uint32_t dst[kMine], code_at[kMine];
+        // a thread's chunks are the same place of rows kStep apart
+        constexpr int kStep = 8 * 16 / kChunksPerRow;
+        const int place = 4 * uw + (lane >> 3);
+        const int pc = place % kChunksPerRow, row0 = (place / kChunksPerRow) * 8 + (lane & 7);
+        const int lc = pc ^ (kv4_swizzle(row0, D / 16) >> 1);  // the dims: 32 lc ..
+        uint32_t dst[4];
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int c = 16 * i + 4 * uw + (lane >> 3);
-            row[i] = (c / kChunksPerRow) * 8 + (lane & 7);
-            const int pc = c % kChunksPerRow;
-            lc[i] = pc ^ (kv4_swizzle(row[i], D / 16) >> 1);
-            code_at[i] = pc * 16;
-            dst[i] = (lc[i] >> 1) * W::kKvBlock;
-        }
+        for (int j = 0; j < 4; ++j) dst[j] = (lc >> 1) * W::kKvBlock + sw128_offset(row0, (lc & 1) * 4 + j);
+        const uint32_t code_off = row0 * (D / 2) + pc * 16, scale_off = psize * (D / 2) + row0 * (D / 16) + 2 * lc;
         WinCursor ahead = cur;   // of the tile whose data is requested next
         int a_r = 0, a_r1 = 0;
         Unit a{};
@@ -520,7 +553,25 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
         uint32_t bad = 0;
         auto fetch = [&]() {
             const int p0 = a_r * kTok;
-            // lane j < 4 looks up page j of the tile (one page, or several of a tile)
+            const uint8_t* head = p.c.cache + (static_cast<size_t>(a.l) * p.c.n_pages * p.c.kv_heads + a.h) * head_bytes;
+            if (shift == 6 && p0 + kTok <= a.end) {  // a whole tile of one page
+                const int page = kv4_page(p.c, a.n, p0);
+                bad = page < 0 ? 15u : 0u;
+                const int in_page = p0 & (psize - 1);
+                const uint8_t* k = head + static_cast<unsigned long long>(static_cast<uint32_t>(max(page, 0))) * page_bytes;
+                const uint8_t* v = k + head_bytes / 2;
+                const uint32_t co = code_off + in_page * (D / 2), so = scale_off + in_page * (D / 16);
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    kc[i] = __ldg(reinterpret_cast<const uint4*>(k + co + i * kStep * (D / 2)));
+                    vc[i] = __ldg(reinterpret_cast<const uint4*>(v + co + i * kStep * (D / 2)));
+                    ks[i] = __ldg(reinterpret_cast<const uint16_t*>(k + so + i * kStep * (D / 16)));
+                    vs[i] = __ldg(reinterpret_cast<const uint16_t*>(v + so + i * kStep * (D / 16)));
+                    if (page < 0) ks[i] = vs[i] = 0u;
+                }
+                return;
+            }
+            // lane j < 4 looks up page j of the tile
             const int pos = p0 + (lane << shift);
             const bool want = lane < (kTok >> shift) && pos < a.end;
             const int page = want ? kv4_page(p.c, a.n, pos) : -2;
@@ -529,34 +580,32 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             bad = 0;
 #pragma unroll
             for (int q = 0; q < 4; ++q) bad |= ((gone >> ((16 * q) >> shift)) & 1u) << q;
-            const uint8_t* head = p.c.cache + (static_cast<size_t>(a.l) * p.c.n_pages * p.c.kv_heads + a.h) * head_bytes;
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
-                const int j = row[i] >> shift;
+                const int row = row0 + i * kStep, j = row >> shift;
                 const int pg = __shfl_sync(~0u, page, j);
                 kc[i] = vc[i] = make_uint4(0u, 0u, 0u, 0u);
                 ks[i] = vs[i] = 0u;
-                if (pg >= 0 && p0 + row[i] < a.end) {
-                    const int in_page = (p0 & (psize - 1)) + row[i] - (j << shift);
+                if (pg >= 0 && p0 + row < a.end) {
+                    const int off = (p0 & (psize - 1)) - (j << shift) + i * kStep;  // rows from row0's offsets
                     const uint8_t* k = head + static_cast<unsigned long long>(static_cast<uint32_t>(pg)) * page_bytes;
                     const uint8_t* v = k + head_bytes / 2;
-                    kc[i] = __ldg(reinterpret_cast<const uint4*>(k + in_page * (D / 2) + code_at[i]));
-                    vc[i] = __ldg(reinterpret_cast<const uint4*>(v + in_page * (D / 2) + code_at[i]));
-                    const int sc = psize * (D / 2) + in_page * (D / 16) + 2 * lc[i];
-                    ks[i] = __ldg(reinterpret_cast<const uint16_t*>(k + sc));
-                    vs[i] = __ldg(reinterpret_cast<const uint16_t*>(v + sc));
+                    kc[i] = __ldg(reinterpret_cast<const uint4*>(k + static_cast<int>(code_off) + off * (D / 2)));
+                    vc[i] = __ldg(reinterpret_cast<const uint4*>(v + static_cast<int>(code_off) + off * (D / 2)));
+                    ks[i] = __ldg(reinterpret_cast<const uint16_t*>(k + static_cast<int>(scale_off) + off * (D / 16)));
+                    vs[i] = __ldg(reinterpret_cast<const uint16_t*>(v + static_cast<int>(scale_off) + off * (D / 16)));
                 }
             }
         };
         // one chunk of 32 values, as fp16 in its swizzled row
-        auto put = [&](unsigned char* tile, const uint4& code, uint32_t scales, int i) {
+        auto put = [&](unsigned char* tile, const uint4& code, uint32_t scales) {
             const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+            const uint32_t s0 = scale_twice(scales, 0), s1 = scale_twice(scales, 1);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t v[4];
-                unpack(w[j], scale_twice(scales, j >> 1), v);
-                *reinterpret_cast<uint4*>(tile + dst[i] + sw128_offset(row[i], (lc[i] & 1) * 4 + j)) =
-                    make_uint4(v[0], v[1], v[2], v[3]);
+                unpack(w[j], j < 2 ? s0 : s1, v);
+                *reinterpret_cast<uint4*>(tile + dst[j]) = make_uint4(v[0], v[1], v[2], v[3]);
             }
         };
         if (more) fetch();
@@ -573,7 +622,7 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                 if (bad != 0) atomicOr(&g_kv4_window_error, kErrBadPage);
             }
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) put(kt, kc[i], ks[i], i);
+            for (int i = 0; i < kMine; ++i) put(kt + i * (kStep / 8) * 1024, kc[i], ks[i]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_local(k_full + 8 * s);
@@ -582,7 +631,7 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                 break;
             }
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) put(vt, vc[i], vs[i], i);
+            for (int i = 0; i < kMine; ++i) put(vt + i * (kStep / 8) * 1024, vc[i], vs[i]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_local(v_full + 8 * s);
@@ -660,54 +709,46 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
     }
 }
 
-// Joins the partial results of the units that several CTAs shared: a block per CTA that such a unit starts in and
-// group of four rows, a warp per row.
+// Joins the partial results of the units that several CTAs shared: a column of blocks for each CTA that such a unit
+// starts in, a warp for each row.
 template <int D>
-__global__ void __launch_bounds__(128) kv4_window_join_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(256) kv4_window_join_kernel(const __grid_constant__ AttnParams p) {
     constexpr size_t kSlot = kRows * (D + 2);
-    const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5);
-    const int pairs = p.c.L * p.c.kv_heads;
-    const long long total = line_length(p, pairs, lane);
-    const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-    long long lo = 0, hi = 0, first = 0, end = 0;
-    WinCursor k{};
-    bool mine = false;
-    if (static_cast<int>(blockIdx.x) < n) {
-        cta_range(total, blockIdx.x, n, lo, hi);
-        k = find(p, pairs, hi - 1, lane);
-        first = hi - 1 - k.at;
-        end = first + k.cost;
-        mine = first + kStartCost >= lo && k.at >= kStartCost && end > hi;
-    }
-    griddep_wait();  // in every block: the grid must not end before the one it follows
-    if (!mine) return;
+    const int lane = threadIdx.x & 31;
+    griddep_wait();
+    const JoinRecord rec = reinterpret_cast<const JoinRecord*>(p.records)[blockIdx.x];
+    if (rec.parts == 0) return;
+    WinCursor k{rec.b, rec.block, rec.pair, 0, 0, 0};
     const Unit x = win_unit(p, k);
-    if (row >= static_cast<long long>(x.n) * p.group - x.col0) return;
-    const int parts = cta_of(total, end - 1, n) - static_cast<int>(blockIdx.x) + 1;
+    const long long rows = static_cast<long long>(x.n) * p.group - x.col0;
     const float* base = p.part + static_cast<size_t>(blockIdx.x) * 2 * kSlot;
     auto slot = [&](int i) -> const float* { return i == 0 ? base + kSlot : base + static_cast<size_t>(i) * 2 * kSlot; };
-    float mm = -INFINITY;
-    for (int i = 0; i < parts; ++i) mm = fmaxf(mm, slot(i)[kRows * D + row]);
-    float2 v[D / 64];
+    for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < min(rows, static_cast<long long>(kRows)); row += gridDim.y * 8) {
+        float mm = -INFINITY;
+        for (int i = lane; i < rec.parts; i += 32) mm = fmaxf(mm, slot(i)[kRows * D + row]);
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
+        float2 v[D / 64];
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) v[c] = make_float2(0.0f, 0.0f);
-    float l = 0.0f;
-    for (int i = 0; i < parts; ++i) {
-        const float* s = slot(i);
-        const float ms = s[kRows * D + row];
-        const float f = ms == -INFINITY ? 0.0f : exp2_approx(ms - mm);
-        l += s[kRows * D + kRows + row] * f;
+        for (int c = 0; c < D / 64; ++c) v[c] = make_float2(0.0f, 0.0f);
+        float l = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < rec.parts; ++i) {
+            const float* s = slot(i);
+            const float ms = s[kRows * D + row];
+            const float f = ms == -INFINITY ? 0.0f : exp2_approx(ms - mm);
+            l += s[kRows * D + kRows + row] * f;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            const float2 y = *reinterpret_cast<const float2*>(s + row * D + 64 * c + 2 * lane);
-            v[c].x += y.x * f;
-            v[c].y += y.y * f;
+            for (int c = 0; c < D / 64; ++c) {
+                const float2 y = *reinterpret_cast<const float2*>(s + row * D + 64 * c + 2 * lane);
+                v[c].x += y.x * f;
+                v[c].y += y.y * f;
+            }
         }
-    }
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    const size_t out = q_row(p, k.b, x, x.col0 + row) + 2 * lane;
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        const size_t out = q_row(p, k.b, x, x.col0 + row) + 2 * lane;
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) store_out2(p, out + 64 * c, v[c].x * inv, v[c].y * inv);
+        for (int c = 0; c < D / 64; ++c) store_out2(p, out + 64 * c, v[c].x * inv, v[c].y * inv);
+    }
 }
 
 constexpr int kMaxSms = 192;  // the workspace is sized for cards of up to as many
@@ -733,8 +774,8 @@ cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const long long rows = std::min<long long>(static_cast<long long>(p.c.T) * p.group, kRows);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, static_cast<unsigned>((rows + 3) / 4));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(ctas, static_cast<unsigned>(std::min<long long>((rows + 7) / 8, 4)));
+    cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -752,11 +793,12 @@ cudaError_t launch_dim(const AttnParams& p, cudaStream_t stream) {
 }  // namespace
 
 size_t kv4_window_workspace_bytes(int head_dim) {
-    return static_cast<size_t>(2 * kMaxSms) * 2 * kRows * (head_dim + 2) * sizeof(float);
+    return static_cast<size_t>(2 * kMaxSms) * (2 * kRows * (head_dim + 2) * sizeof(float) + sizeof(JoinRecord));
 }
 
 cudaError_t launch_kv4_window(AttnParams p, cudaStream_t stream) {
     p.col_blocks = static_cast<int>((static_cast<long long>(p.c.T) * p.group + kRows - 1) / kRows);
+    p.records = p.part + static_cast<size_t>(2 * kMaxSms) * 2 * kRows * (p.c.head_dim + 2);
     switch (p.c.head_dim) {
         case 64: return launch_dim<64>(p, stream);
         case 128: return launch_dim<128>(p, stream);
