@@ -67,7 +67,7 @@ struct Win {
     static constexpr uint32_t kOffBad = kOffMul + kRows * 4;         // missing pages of tiles j mod 4
     static constexpr uint32_t kOffXch = kOffBad + 4 * 4;             // what the two halves of a row tell each other
     static constexpr uint32_t kOffBar = kOffXch + 2 * 2 * kRows * 4;
-    static constexpr uint32_t kBars = 2 + 2 + 2 + 2 + 2 + 1 + 1 + 4;  // see below
+    static constexpr uint32_t kBars = 2 + 2 + 2 + 2 + 2 + 1 + 1;      // see below
     static constexpr uint32_t kUsed = kOffBar + kBars * 8 + 64;      // + cursor, tensor memory address
     static constexpr int kCtas = D <= 128 && 2 * (kUsed + 2048) <= 232448 ? 2 : 1;
     // no more CTAs than the tensor memory has room for: a third (second) would wait in its allocation
@@ -249,9 +249,29 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 
+// Waits for phase `parity` of the mbarrier, giving up after kWaitLimitNs. The hardware suspends the thread for up to
+// 20 us at a time: five waits per tile and warp that polled took a tenth of the SM's issue slots.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+    unsigned long long t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        const unsigned long long t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitLimitNs) return false;
+    }
+}
+
 // Every lane of a warp waits; false, for all of them, if one gave up.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    const bool late = !mbar_wait_bounded(bar, parity);
+    const bool late = !wait_for(bar, parity);
     return !__any_sync(~0u, late);
 }
 
@@ -271,7 +291,7 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
     const uint32_t bars = base + W::kOffBar;
     const uint32_t k_full = bars, v_full = bars + 16;      // per stage: unpacked
     const uint32_t s_done = bars + 32, p_ready = bars + 48, o_done = bars + 64;  // per parity of the tile
-    const uint32_t q_full = bars + 80, drained = bars + 88, pair = bars + 96;  // pair: per 32 rows
+    const uint32_t q_full = bars + 80, drained = bars + 88;
     float* xch = reinterpret_cast<float*>(sm + W::kOffXch);
     const int pairs = p.c.L * p.c.kv_heads;
 
@@ -300,7 +320,6 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
         }
         mbar_init(q_full, kSoftWarps);
         mbar_init(drained, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(pair + 8 * i, 2);
         fence_mbar_init();
     }
     __syncthreads();
@@ -326,22 +345,17 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
         const int quarter = warp & 3, half = warp >> 2;
         const int row = 32 * quarter + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-        const uint32_t my_pair = pair + 8 * quarter;
-        uint32_t met = 0;  // times the two halves have met
-        // This half's value of the row to the other half, and the other's value here.
-        auto exchange = [&](float v, float& other) -> bool {
+        int met = 0;  // times the two halves have met
+        // This half's value of the row to the other half; returns the other's. A warp that has given up waiting still comes
+        // here as often as its other half does, so this barrier needs no limit of its own.
+        auto exchange = [&](float v) -> float {
             float* x = xch + (met & 1) * 2 * kRows + row;
-            x[half * kRows] = v;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_local(my_pair);
-            if (!warp_wait(my_pair, met & 1)) return false;
-            tc_fence_after();
             ++met;
-            other = x[(half ^ 1) * kRows];
-            return true;
+            x[half * kRows] = v;
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+            return x[(half ^ 1) * kRows];
         };
-        for (; cur.left > 0 && !failed; next_unit(p, pairs, cur)) {
+        for (; cur.left > 0; next_unit(p, pairs, cur)) {
             int r0, r1;
             unit_tiles(cur, r0, r1);
             if (r1 <= r0) break;
@@ -383,11 +397,7 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_local(q_full);
-            float other;
-            if (!exchange(0.0f, other)) {  // the other half's rows have their factors
-                failed = true;
-                break;
-            }
+            (void)exchange(0.0f);  // the other half's rows have their factors
 
             const bool some = 32 * quarter < rows;  // this warp has rows
             const float mul = row < rows ? mul_s[row] : kLeastScale;
@@ -395,17 +405,14 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             const int seen_by_all = min(x.start + x.col0 / p.group + 1, x.end);
             float m = -INFINITY, shift = kNone, l = 0.0f;
             for (int r = r0; r < r1; ++r, ++n) {
-                if (!warp_wait(s_done + 8 * (n & 1), tile_parity(n))) {
-                    failed = true;
-                    break;
-                }
+                if (!failed && !warp_wait(s_done + 8 * (n & 1), tile_parity(n))) failed = true;
                 tc_fence_after();
                 if (some) {
-                    const uint32_t s_at = lanes + 64 * (n & 1);
+                    const uint32_t s_at = lanes + 64 * (n & 1) + 32 * half;  // the half's scores, then probabilities
                     const int p0 = r * kTok + 32 * half;  // this half's first position
                     const uint32_t bad = bad_s[n & 3] >> (2 * half);
                     float s[32];
-                    tmem_read32(s_at + 32 * half, s);
+                    tmem_read32(s_at, s);
                     if (p0 + 32 > seen_by_all || bad != 0) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -415,11 +422,7 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
 #pragma unroll
                     for (int i = 4; i < 32; ++i) t[i & 3] = fmaxf(t[i & 3], s[i]);
                     float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-                    if (!exchange(top, other)) {  // after it both halves have read their scores
-                        failed = true;
-                        break;
-                    }
-                    top = fmaxf(top, other);
+                    top = fmaxf(top, exchange(top));
                     if (__any_sync(~0u, fmaf(top, mul, shift) > kPShift + kSlack)) {
                         const float v = fmaxf(m, top * mul);
                         const float al = v == m ? 1.0f : exp2_approx(m - v);
@@ -427,10 +430,7 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                         shift = v == -INFINITY ? kNone : kPShift - v;
                         l *= al;
                         if (r > r0) {  // this half of the sums so far: after the product that is adding to them
-                            if (!warp_wait(o_done + 8 * ((n - 1) & 1), tile_parity(n - 1))) {
-                                failed = true;
-                                break;
-                            }
+                            if (!failed && !warp_wait(o_done + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
                             tc_fence_after();
 #pragma unroll 1
                             for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
@@ -453,11 +453,11 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                         hi[i] = pack_half2(s[2 * i], s[2 * i + 1]);
                     }
                     l += sum[0] + sum[1];
-                    tmem_st16(s_at + 16 * half, hi);
+                    tmem_st16(s_at, hi);
                     if constexpr (SPLIT) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) hi[i] = pack_rest(s[2 * i], s[2 * i + 1], hi[i]);
-                        tmem_st16(s_at + 32 + 16 * half, hi);
+                        tmem_st16(s_at + 16, hi);
                     }
                     tmem_st_wait();
                 }
@@ -465,13 +465,10 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_local(p_ready + 8 * (n & 1));
             }
-            if (failed) break;
             // outputs: each half its dims
-            if (!exchange(l, other) || !warp_wait(o_done + 8 * ((n - 1) & 1), tile_parity(n - 1))) {
-                failed = true;
-                break;
-            }
+            const float other = exchange(l);
             l = half == 0 ? l + other : other + l;
+            if (!failed && !warp_wait(o_done + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
             tc_fence_after();
             const bool done = r0 == 0 && r1 == cur.cost - kStartCost;
             if (some) {
@@ -525,7 +522,9 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
         const uint32_t code_off = row0 * (D / 2) + pc * 16, scale_off = psize * (D / 2) + row0 * (D / 16) + 2 * lc;
         WinCursor ahead = cur;   // of the tile whose data is requested next
         int a_r = 0, a_r1 = 0;
-        Unit a{};
+        int a_end = 0;
+        const int32_t* a_table = nullptr;  // the sequence's pages
+        const uint8_t* a_head = nullptr;
         bool more = true;
         // steps to the next tile; false at the end of the CTA's places
         auto step = [&]() {
@@ -537,12 +536,13 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                 }
                 int r0, r1;
                 unit_tiles(ahead, r0, r1);
-                a = win_unit(p, ahead);
+                const Unit x = win_unit(p, ahead);
                 a_r = r0;
                 a_r1 = r1;
-                const int b = ahead.b;
+                a_end = x.end;
+                a_table = p.c.block_table + static_cast<size_t>(ahead.b) * p.c.max_pages;
+                a_head = p.c.cache + (static_cast<size_t>(x.l) * p.c.n_pages * p.c.kv_heads + x.h) * head_bytes;
                 next_unit(p, pairs, ahead);
-                a.n = b;  // (the sequence; its token count is not needed here)
                 if (r1 > r0) return;
             }
         };
@@ -553,12 +553,12 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
         uint32_t bad = 0;
         auto fetch = [&]() {
             const int p0 = a_r * kTok;
-            const uint8_t* head = p.c.cache + (static_cast<size_t>(a.l) * p.c.n_pages * p.c.kv_heads + a.h) * head_bytes;
-            if (shift == 6 && p0 + kTok <= a.end) {  // a whole tile of one page
-                const int page = kv4_page(p.c, a.n, p0);
+            if (shift == 6 && p0 + kTok <= a_end) {  // a whole tile of one page
+                int page = __ldg(a_table + (p0 >> p.c.page_shift));
+                if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.n_pages)) page = -1;
                 bad = page < 0 ? 15u : 0u;
                 const int in_page = p0 & (psize - 1);
-                const uint8_t* k = head + static_cast<unsigned long long>(static_cast<uint32_t>(max(page, 0))) * page_bytes;
+                const uint8_t* k = a_head + static_cast<unsigned long long>(static_cast<uint32_t>(max(page, 0))) * page_bytes;
                 const uint8_t* v = k + head_bytes / 2;
                 const uint32_t co = code_off + in_page * (D / 2), so = scale_off + in_page * (D / 16);
 #pragma unroll
@@ -573,8 +573,9 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             }
             // lane j < 4 looks up page j of the tile
             const int pos = p0 + (lane << shift);
-            const bool want = lane < (kTok >> shift) && pos < a.end;
-            const int page = want ? kv4_page(p.c, a.n, pos) : -2;
+            const bool want = lane < (kTok >> shift) && pos < a_end;
+            int page = want ? __ldg(a_table + (pos >> p.c.page_shift)) : 0;
+            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.n_pages)) page = -1;
             const unsigned gone = __ballot_sync(~0u, page == -1);
             // the missing pages as 16-token groups, whatever the page size
             bad = 0;
@@ -586,9 +587,9 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                 const int pg = __shfl_sync(~0u, page, j);
                 kc[i] = vc[i] = make_uint4(0u, 0u, 0u, 0u);
                 ks[i] = vs[i] = 0u;
-                if (pg >= 0 && p0 + row < a.end) {
+                if (pg >= 0 && p0 + row < a_end) {
                     const int off = (p0 & (psize - 1)) - (j << shift) + i * kStep;  // rows from row0's offsets
-                    const uint8_t* k = head + static_cast<unsigned long long>(static_cast<uint32_t>(pg)) * page_bytes;
+                    const uint8_t* k = a_head + static_cast<unsigned long long>(static_cast<uint32_t>(pg)) * page_bytes;
                     const uint8_t* v = k + head_bytes / 2;
                     kc[i] = __ldg(reinterpret_cast<const uint4*>(k + static_cast<int>(code_off) + off * (D / 2)));
                     vc[i] = __ldg(reinterpret_cast<const uint4*>(v + static_cast<int>(code_off) + off * (D / 2)));
@@ -646,17 +647,17 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
         // O += P V of tile t
         auto second = [&](int t, bool first) -> bool {
             const int s = t % kStages;
-            if (!mbar_wait_bounded(v_full + 8 * s, stage_parity(t))) return false;
-            if (!mbar_wait_bounded(p_ready + 8 * (t & 1), tile_parity(t))) return false;
+            if (!wait_for(v_full + 8 * s, stage_parity(t))) return false;
+            if (!wait_for(p_ready + 8 * (t & 1), tile_parity(t))) return false;
             tc_fence_after();
             const uint32_t v = base + W::kOffV + s * W::kKvBytes;
 #pragma unroll
             for (int kk = 0; kk < kTok / 16; ++kk) {
-                mma_f16_ta(tmem + W::kTmO, tmem + 64 * (t & 1) + 8 * kk, sw128_mn_desc(v + kk * 2048, W::kKvBlock), idesc_o,
-                           first && kk == 0 ? 0u : 1u);
+                // 32 tokens' probabilities from column 0 (their rests from 16), the other 32's from column 32
+                const uint32_t pr = tmem + 64 * (t & 1) + 32 * (kk >> 1) + 8 * (kk & 1);
+                mma_f16_ta(tmem + W::kTmO, pr, sw128_mn_desc(v + kk * 2048, W::kKvBlock), idesc_o, first && kk == 0 ? 0u : 1u);
                 if constexpr (SPLIT)
-                    mma_f16_ta(tmem + W::kTmO, tmem + 64 * (t & 1) + 32 + 8 * kk, sw128_mn_desc(v + kk * 2048, W::kKvBlock),
-                               idesc_o, 1u);
+                    mma_f16_ta(tmem + W::kTmO, pr + 16, sw128_mn_desc(v + kk * 2048, W::kKvBlock), idesc_o, 1u);
             }
             mma_commit(o_done + 8 * (t & 1));
             return true;
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             int r0, r1;
             unit_tiles(cur, r0, r1);
             if (r1 <= r0) break;
-            if (!mbar_wait_bounded(q_full, static_cast<uint32_t>(units) & 1u)) {
+            if (!wait_for(q_full, static_cast<uint32_t>(units) & 1u)) {
                 failed = true;
                 break;
             }
@@ -673,8 +674,8 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             for (int r = r0; r < r1 && !failed; ++r, ++n) {
                 const int s = n % kStages;
                 // (the buffer's last reader, the second product of tile n - 2, has completed)
-                if (!mbar_wait_bounded(k_full + 8 * s, stage_parity(n)) ||
-                    (n >= 2 && !mbar_wait_bounded(o_done + 8 * (n & 1), tile_parity(n - 2)))) {
+                if (!wait_for(k_full + 8 * s, stage_parity(n)) ||
+                    (n >= 2 && !wait_for(o_done + 8 * (n & 1), tile_parity(n - 2)))) {
                     failed = true;
                     break;
                 }
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
         }
         // whatever was issued has completed before the tensor memory is freed
         mma_commit(drained);
-        (void)mbar_wait_bounded(drained, 0);
+        (void)wait_for(drained, 0);
     }
     if (failed && lane == 0) atomicOr(&g_kv4_window_error, kErrWaitTimeout);
     __syncwarp();
