@@ -24,6 +24,7 @@ struct AttnParams {
     float* part;    // per CTA two partial results: [columns][D] sums, then maxima and sums of the columns
     void* records;  // per CTA a JoinRecord
     int q_heads, group, col_blocks;
+    int unit_rows;  // of the window kernel's units
     DType dtype;
     float scale_log2;
 };

@@ -11,14 +11,14 @@
 // pipe, and unpacking and softmax about 500 issue slots of each of its four schedulers; the roles below
 // overlap the three, and two CTAs per SM (D <= 128) fill each other's waits.
 //
-//   warps 0-7  half a row per thread (warps w and w + 4 share rows and exchange their
+//   warp 0     issues the products (the first warp: the schedulers seem to prefer older ones, and everything waits for it)
+//   8 warps    half a row per thread (for each 128 rows; warps w and w + 4 share rows and exchange their
 //              halves' maxima): queries in, the softmax of a tile from tensor
 //              memory, probabilities back to tensor memory (fp16, over the scores they
 //              came from, as the A operand of the second product), outputs out
-//   warps 8-11 unpack the next tiles: 16 bytes of codes per thread from global
+//   4-8 warps  unpack the next tiles: 16 bytes of codes per thread from global
 //              memory, a tile ahead in registers, to fp16 in the swizzled
 //              K-major rows that both products read (V with its rows as K: MN-major)
-//   warp 12    issues the products
 //
 // Scores have two buffers in tensor memory, K and V tiles two stages each, so
 // the product of tile j + 1 runs during the softmax of tile j. The
@@ -46,35 +46,40 @@ namespace {
 
 constexpr int kRows = 128;       // of a block
 constexpr int kTok = 64;         // of a tile
-constexpr int kSoftWarps = 8, kUnpackWarps = 4;
-constexpr int kIssueWarp = kSoftWarps + kUnpackWarps;
-constexpr int kWinThreads = 32 * (kSoftWarps + kUnpackWarps + 1);
 constexpr int kStartCost = 4;    // places of a block's start on the line, in tiles
 
 __device__ unsigned int g_kv4_window_error = 0;
 
-template <int D, bool SPLIT>
+// NB blocks of 128 rows per CTA share the unpacked tiles: two where a window has as many rows and the tensor memory
+// has room for their sums (D <= 128), one CTA per SM then; otherwise one, and two CTAs per SM where they fit.
+template <int D, bool SPLIT, int NB>
 struct Win {
+    static constexpr int kSoftWarps = 8 * NB;
+    static constexpr int kUnpackWarps = D == 128 ? 4 * NB : 4;
+    static constexpr int kThreads = 32 * (1 + kSoftWarps + kUnpackWarps);
+    static constexpr int kUnitRows = NB * kRows;
     static constexpr int kStages = D == 256 && SPLIT ? 1 : 2;
     static constexpr int kBlk = D / 64;                        // 64-dim blocks of a row (128 bytes)
     static constexpr uint32_t kQBlock = kRows * 128;           // bytes of a block of Q
-    static constexpr uint32_t kQBytes = kBlk * kQBlock;        // of Q hi (then lo)
+    static constexpr uint32_t kQBytes = kBlk * kQBlock;        // of Q hi (then lo) of 128 rows
+    static constexpr uint32_t kQRows = kQBytes * (SPLIT ? 2 : 1);
     static constexpr uint32_t kKvBlock = kTok * 128;           // of a block of K or V
     static constexpr uint32_t kKvBytes = kBlk * kKvBlock;
-    static constexpr uint32_t kOffK = kQBytes * (SPLIT ? 2 : 1);
+    static constexpr uint32_t kOffK = kQRows * NB;
     static constexpr uint32_t kOffV = kOffK + kStages * kKvBytes;
     static constexpr uint32_t kOffMul = kOffV + kStages * kKvBytes;  // factor of a row's raw scores
-    static constexpr uint32_t kOffBad = kOffMul + kRows * 4;         // missing pages of tiles j mod 4
+    static constexpr uint32_t kOffBad = kOffMul + kUnitRows * 4;     // missing pages of tiles j mod 4
     static constexpr uint32_t kOffXch = kOffBad + 4 * 4;             // what the two halves of a row tell each other
-    static constexpr uint32_t kOffBar = kOffXch + 2 * 2 * kRows * 4;
-    static constexpr uint32_t kBars = 2 + 2 + 2 + 2 + 2 + 1 + 1;      // see below
+    static constexpr uint32_t kOffBar = kOffXch + 2 * 2 * kUnitRows * 4;
+    static constexpr uint32_t kBars = 2 + 2 + 2 * NB + 2 * NB + 2 + 1 + 1;  // see below
     static constexpr uint32_t kUsed = kOffBar + kBars * 8 + 64;      // + cursor, tensor memory address
-    static constexpr int kCtas = D <= 128 && 2 * (kUsed + 2048) <= 232448 ? 2 : 1;
+    static constexpr int kCtas = NB == 1 && D <= 128 && 2 * (kUsed + 2048) <= 232448 ? 2 : 1;
     // no more CTAs than the tensor memory has room for: a third (second) would wait in its allocation
     static constexpr uint32_t kLeast = kCtas == 2 ? 80 * 1024 : 118 * 1024;
     static constexpr uint32_t kSmem = (kUsed + 1024 > kLeast ? kUsed + 1024 : kLeast);
-    static constexpr uint32_t kTmCols = D == 256 ? 512 : 256;
-    static constexpr uint32_t kTmO = 128;                            // scores at 0 and 64
+    static constexpr uint32_t kTmCols = NB * (128 + D) <= 256 ? 256 : 512;
+    static constexpr uint32_t kTmO = NB * 128;                       // scores of block i at 128 i, + 64
+    static_assert(NB * (128 + D) <= 512, "scores and sums fit the tensor memory");
 };
 
 // Where a CTA is: unit (b, block, pair of layer and kv head), at place `at` of its `cost`, `left` places to go.
@@ -85,9 +90,9 @@ struct WinCursor {
 
 // First position that no row of block blk sees (0: no row).
 __device__ __forceinline__ int block_end(const AttnParams& p, const Kv4Window& w, int blk) {
-    const long long row = static_cast<long long>(blk) * kRows;
-    if (row >= static_cast<long long>(w.n) * p.group) return 0;
-    const int t_hi = static_cast<int>(min((row + kRows - 1) / p.group, static_cast<long long>(w.n) - 1));
+    const int row = blk * p.unit_rows;  // T group < 2^31
+    if (row >= w.n * p.group) return 0;
+    const int t_hi = min(static_cast<int>((static_cast<uint32_t>(row) + p.unit_rows - 1) / p.group), w.n - 1);
     return w.start + min(t_hi + 1, w.cap - w.start);
 }
 
@@ -163,7 +168,7 @@ __device__ __forceinline__ Unit win_unit(const AttnParams& p, const WinCursor& k
     const Kv4Window w = kv4_window(p.c, k.b);
     x.h = k.lh % p.c.kv_heads;
     x.l = k.lh / p.c.kv_heads;
-    x.col0 = k.blk * kRows;
+    x.col0 = k.blk * p.unit_rows;
     x.start = w.start;
     x.n = w.n;
     x.end = block_end(p, w, k.blk);
@@ -175,14 +180,35 @@ __host__ __device__ constexpr uint32_t idesc_f16(int n) {
     return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
 }
 
-// A from tensor memory (fp16 pairs, 8 columns of 32 bits per k-step of 16).
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// One product step, D (tensor memory) = or += A B, with the descriptors' halves apart: their upper halves are one
+// constant and their lower ones differ by constants, so a step costs the issuing thread an addition or two.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart, version, 128-byte swizzle
+
+// Lower halves: K-major rows, and rows read as K (MN-major) with 64-wide blocks `stride` bytes apart.
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t stride) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((stride >> 4) << 16);
+}
+
+template <bool FIRST>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(kDescHi), "n"(FIRST ? 0 : 1)
+        : "memory");
+}
+
+// A from tensor memory (fp16 pairs, 8 columns of 32 bits per k-step of 16).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %4};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(idesc), "r"(kDescHi), "r"(accumulate)
         : "memory");
 }
 
@@ -239,6 +265,12 @@ __device__ __forceinline__ void store_out16(const AttnParams& p, size_t i, const
     out[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Stores 16 consecutive columns of this warp's lanes, one lane per thread.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
@@ -247,6 +279,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 // Waits for phase `parity` of the mbarrier, giving up after kWaitLimitNs. The hardware suspends the thread for up to
@@ -275,11 +314,12 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return !__any_sync(~0u, late);
 }
 
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
+template <int D, bool SPLIT, int NB>
+__global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>::kCtas)
     kv4_window_kernel(const __grid_constant__ AttnParams p) {
-    using W = Win<D, SPLIT>;
-    constexpr int kStages = W::kStages;
+    using W = Win<D, SPLIT, NB>;
+    constexpr int kStages = W::kStages, kSoftWarps = W::kSoftWarps, kUnpackWarps = W::kUnpackWarps;
+    constexpr int kUnitRows = W::kUnitRows;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
     unsigned char* sm = smem_raw + (base - raw);
@@ -290,18 +330,19 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(cur_s + 1);
     const uint32_t bars = base + W::kOffBar;
     const uint32_t k_full = bars, v_full = bars + 16;      // per stage: unpacked
-    const uint32_t s_done = bars + 32, p_ready = bars + 48, o_done = bars + 64;  // per parity of the tile
-    const uint32_t q_full = bars + 80, drained = bars + 88;
+    const uint32_t o_done = bars + 32;                     // per parity of the tile
+    const uint32_t q_full = bars + 48, drained = bars + 56;
+    const uint32_t s_done = bars + 64, p_ready = s_done + 16 * NB;  // per block and parity
     float* xch = reinterpret_cast<float*>(sm + W::kOffXch);
     const int pairs = p.c.L * p.c.kv_heads;
 
     long long total = 0;
     int ctas = 0;
-    if (warp == 0 || warp == kIssueWarp) {
+    if (warp < 2) {
         total = line_length(p, pairs, lane);
         ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
     }
-    if (warp == kIssueWarp) {
+    if (warp == 0) {
         long long lo = 0, hi = 0;
         WinCursor k{};
         if (static_cast<int>(blockIdx.x) < ctas) {
@@ -310,13 +351,15 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
         }
         k.left = static_cast<int>(hi - lo);
         if (lane == 0) *cur_s = k;
-    } else if (tid == 0) {
+    } else if (tid == 32) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(k_full + 8 * i, kUnpackWarps);
             mbar_init(v_full + 8 * i, kUnpackWarps);
-            mbar_init(s_done + 8 * i, 1);
-            mbar_init(p_ready + 8 * i, kSoftWarps);
             mbar_init(o_done + 8 * i, 1);
+            for (int j = 0; j < NB; ++j) {
+                mbar_init(s_done + 16 * j + 8 * i, 1);
+                mbar_init(p_ready + 16 * j + 8 * i, 8);
+            }
         }
         mbar_init(q_full, kSoftWarps);
         mbar_init(drained, 1);
@@ -326,7 +369,7 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
     WinCursor cur = *cur_s;
     griddep_launch_dependents();
     JoinRecord* record = reinterpret_cast<JoinRecord*>(p.records) + blockIdx.x;
-    if (tid == 0) *record = JoinRecord{0, 0, 0, 0};
+    if (tid == 32) *record = JoinRecord{0, 0, 0, 0};
     if (cur.left <= 0) return;
     if (warp == 0) tmem_alloc(smem_addr(tmem_s), W::kTmCols);
     tc_fence_before();
@@ -340,20 +383,21 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
     bool failed = false;
     int n = 0;
 
-    if (warp < kSoftWarps) {
+    if (warp > 0 && warp <= kSoftWarps) {
         // ------------------------------------------------------------------ rows
-        const int quarter = warp & 3, half = warp >> 2;
-        const int row = 32 * quarter + lane;
+        const int block = (warp - 1) >> 3, quarter = warp & 3, half = ((warp - 1) >> 2) & 1;  // (a warp reaches lanes 32 (warp mod 4) ..)
+        const int row = 128 * block + 32 * quarter + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+        const uint32_t o_at = lanes + W::kTmO + block * D;  // the row's sums
         int met = 0;  // times the two halves have met
         // This half's value of the row to the other half; returns the other's. A warp that has given up waiting still comes
         // here as often as its other half does, so this barrier needs no limit of its own.
         auto exchange = [&](float v) -> float {
-            float* x = xch + (met & 1) * 2 * kRows + row;
+            float* x = xch + (met & 1) * 2 * kUnitRows + row;
             ++met;
-            x[half * kRows] = v;
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-            return x[(half ^ 1) * kRows];
+            x[half * kUnitRows] = v;
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * block + quarter) : "memory");
+            return x[(half ^ 1) * kUnitRows];
         };
         for (; cur.left > 0; next_unit(p, pairs, cur)) {
             int r0, r1;
@@ -361,12 +405,12 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             if (r1 <= r0) break;
             const Unit x = win_unit(p, cur);
             const int b = cur.b;
-            const int rows = static_cast<int>(min(static_cast<long long>(x.n) * p.group - x.col0, static_cast<long long>(kRows)));
-            if (tid == 0 && x.n > kv4_window(p.c, b).cap - x.start) atomicOr(&g_kv4_window_error, kErrBadPage);
+            const int rows = min(x.n * p.group - x.col0, kUnitRows);
+            if (tid == 32 && x.n > kv4_window(p.c, b).cap - x.start) atomicOr(&g_kv4_window_error, kErrBadPage);
             // queries of half of these rows, scaled to fill fp16's range
 #pragma unroll 2
             for (int i = 0; i < 16; ++i) {
-                const int rr = 32 * quarter + 16 * half + i;
+                const int rr = 128 * block + 32 * quarter + 16 * half + i;
                 if (rr >= rows) break;
                 constexpr int kChunks = D > 128 ? D / 128 : 1;
                 float4 v[kChunks];
@@ -385,7 +429,7 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                 for (int c = 0; c < kChunks; ++c) {
                     const int d = 4 * lane + 128 * c;
                     if (d >= D) continue;
-                    const uint32_t at = (d >> 6) * W::kQBlock + sw128_offset(rr, (d & 63) >> 3) + (d & 7) * 2;
+                    const uint32_t at = block * W::kQRows + (d >> 6) * W::kQBlock + sw128_offset(rr & 127, (d & 63) >> 3) + (d & 7) * 2;
                     const float q0 = v[c].x * f, q1 = v[c].y * f, q2 = v[c].z * f, q3 = v[c].w * f;
                     const uint2 hi = make_uint2(pack_half2(q0, q1), pack_half2(q2, q3));
                     *reinterpret_cast<uint2*>(sm + at) = hi;
@@ -399,16 +443,16 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             if (lane == 0) mbar_arrive_local(q_full);
             (void)exchange(0.0f);  // the other half's rows have their factors
 
-            const bool some = 32 * quarter < rows;  // this warp has rows
+            const bool some = 128 * block + 32 * quarter < rows;  // this warp has rows
             const float mul = row < rows ? mul_s[row] : kLeastScale;
             const int lim = row < rows ? min(x.start + (x.col0 + row) / p.group, x.end - 1) : -1;
             const int seen_by_all = min(x.start + x.col0 / p.group + 1, x.end);
             float m = -INFINITY, shift = kNone, l = 0.0f;
             for (int r = r0; r < r1; ++r, ++n) {
-                if (!failed && !warp_wait(s_done + 8 * (n & 1), tile_parity(n))) failed = true;
+                if (!failed && !warp_wait(s_done + 16 * block + 8 * (n & 1), tile_parity(n))) failed = true;
                 tc_fence_after();
                 if (some) {
-                    const uint32_t s_at = lanes + 64 * (n & 1) + 32 * half;  // the half's scores, then probabilities
+                    const uint32_t s_at = lanes + 128 * block + 64 * (n & 1) + 32 * half;  // the half's scores, then probabilities
                     const int p0 = r * kTok + 32 * half;  // this half's first position
                     const uint32_t bad = bad_s[n & 3] >> (2 * half);
                     float s[32];
@@ -418,10 +462,13 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                         for (int i = 0; i < 32; ++i)
                             if (p0 + i > lim || ((bad >> (i >> 4)) & 1u)) s[i] = -INFINITY;
                     }
-                    float t[4] = {s[0], s[1], s[2], s[3]};
+                    float t0 = max3(s[0], s[1], s[2]), t1 = max3(s[3], s[4], s[5]);
 #pragma unroll
-                    for (int i = 4; i < 32; ++i) t[i & 3] = fmaxf(t[i & 3], s[i]);
-                    float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                    for (int i = 6; i < 30; i += 4) {
+                        t0 = max3(t0, s[i], s[i + 1]);
+                        t1 = max3(t1, s[i + 2], s[i + 3]);
+                    }
+                    float top = fmaxf(max3(t0, s[30], s[31]), t1);
                     top = fmaxf(top, exchange(top));
                     if (__any_sync(~0u, fmaf(top, mul, shift) > kPShift + kSlack)) {
                         const float v = fmaxf(m, top * mul);
@@ -435,24 +482,25 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
 #pragma unroll 1
                             for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
                                 uint32_t w[16];
-                                tmem_read16(lanes + W::kTmO + c, w);
+                                tmem_read16(o_at + c, w);
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * al);
-                                tmem_st16(lanes + W::kTmO + c, w);
+                                tmem_st16(o_at + c, w);
                             }
                         }
                     }
-                    float sum[2] = {0.0f, 0.0f};
+                    float2 sum = make_float2(0.0f, 0.0f);
+                    const float2 mul2 = make_float2(mul, mul), shift2 = make_float2(shift, shift);
                     uint32_t hi[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        s[2 * i] = exp2_approx(fmaf(s[2 * i], mul, shift));
-                        s[2 * i + 1] = exp2_approx(fmaf(s[2 * i + 1], mul, shift));
-                        sum[0] += s[2 * i];
-                        sum[1] += s[2 * i + 1];
+                        const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), mul2, shift2);
+                        s[2 * i] = exp2_approx(e.x);
+                        s[2 * i + 1] = exp2_approx(e.y);
+                        sum = __fadd2_rn(sum, make_float2(s[2 * i], s[2 * i + 1]));
                         hi[i] = pack_half2(s[2 * i], s[2 * i + 1]);
                     }
-                    l += sum[0] + sum[1];
+                    l += sum.x + sum.y;
                     tmem_st16(s_at, hi);
                     if constexpr (SPLIT) {
 #pragma unroll
@@ -463,7 +511,7 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_local(p_ready + 8 * (n & 1));
+                if (lane == 0) mbar_arrive_local(p_ready + 16 * block + 8 * (n & 1));
             }
             // outputs: each half its dims
             const float other = exchange(l);
@@ -472,14 +520,14 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             tc_fence_after();
             const bool done = r0 == 0 && r1 == cur.cost - kStartCost;
             if (some) {
-                float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kRows * (D + 2));
+                float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kUnitRows * (D + 2));
                 const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // no key at all: zeros
                 const size_t out = row < rows ? q_row(p, b, x, x.col0 + row) : 0;
 #pragma unroll 1
                 for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
                     uint32_t w[16];
                     __syncwarp();
-                    tmem_read16(lanes + W::kTmO + c, w);
+                    tmem_read16(o_at + c, w);
                     float o[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(w[i]);
@@ -492,27 +540,27 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                     }
                 }
                 if (!done && half == 0 && row < rows) {
-                    slot[kRows * D + row] = m;
-                    slot[kRows * D + kRows + row] = l;
+                    slot[kUnitRows * D + row] = m;
+                    slot[kUnitRows * D + kUnitRows + row] = l;
                 }
                 __syncwarp();
             }
-            if (tid == 0 && !done && r0 == 0)  // this CTA's block of the join has it
+            if (tid == 32 && !done && r0 == 0)  // this CTA's block of the join has it
                 *record = JoinRecord{cur.b, cur.blk, cur.lh,
                                      cta_of(total, mul_div(total, blockIdx.x + 1, ctas) - cur.at - cur.left + cur.cost - 1, ctas) -
                                          static_cast<int>(blockIdx.x) + 1};
             tc_fence_before();
         }
-    } else if (warp < kSoftWarps + kUnpackWarps) {
+    } else if (warp > kSoftWarps) {
         // ---------------------------------------------------------------- unpack
         constexpr int kChunksPerRow = D / 32;            // 16 bytes of codes: 32 dims, two scales
-        constexpr int kMine = D / 64;                    // chunks of K (and of V) per thread
-        const int uw = warp - kSoftWarps;
+        constexpr int kMine = 2 * kChunksPerRow / kUnpackWarps;  // chunks of K (and of V) per thread
+        const int uw = warp - 1 - kSoftWarps;
         const int psize = 1 << p.c.page_shift;
         const int shift = min(p.c.page_shift, 6);
         const uint32_t head_bytes = static_cast<uint32_t>(kv4_head_bytes(psize, D)), page_bytes = head_bytes * p.c.kv_heads;
         // a thread's chunks are the same place of rows kStep apart
-        constexpr int kStep = 8 * 16 / kChunksPerRow;
+        constexpr int kStep = 8 * (4 * kUnpackWarps / kChunksPerRow);
         const int place = 4 * uw + (lane >> 3);
         const int pc = place % kChunksPerRow, row0 = (place / kChunksPerRow) * 8 + (lane & 7);
         const int lc = pc ^ (kv4_swizzle(row0, D / 16) >> 1);  // the dims: 32 lc ..
@@ -612,13 +660,13 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
         if (more) fetch();
         while (more) {
             const int s = n % kStages;
-            if (n >= kStages && !warp_wait(s_done + 8 * ((n - kStages) & 1), tile_parity(n - kStages))) {
+            if (n >= kStages && !warp_wait(s_done + 16 * (NB - 1) + 8 * ((n - kStages) & 1), tile_parity(n - kStages))) {
                 failed = true;
                 break;
             }
             unsigned char* kt = sm + W::kOffK + s * W::kKvBytes;
             unsigned char* vt = sm + W::kOffV + s * W::kKvBytes;
-            if (warp == kSoftWarps && lane == 0) {
+            if (uw == 0 && lane == 0) {
                 bad_s[n & 3] = bad;
                 if (bad != 0) atomicOr(&g_kv4_window_error, kErrBadPage);
             }
@@ -640,24 +688,27 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
             step();
             if (more) fetch();
         }
-    } else if (lane == 0) {
+    } else if (elect_one()) {
         // -------------------------------------------------------------- products
         const uint32_t idesc_s = idesc_f16(kTok), idesc_o = idesc_f16(D) | kIdescBMnMajor;
+        const uint32_t q_desc = desc_k(base), k_desc = desc_k(base + W::kOffK), v_desc = desc_mn(base + W::kOffV, W::kKvBlock);
         int units = 0;
         // O += P V of tile t
         auto second = [&](int t, bool first) -> bool {
             const int s = t % kStages;
             if (!wait_for(v_full + 8 * s, stage_parity(t))) return false;
-            if (!wait_for(p_ready + 8 * (t & 1), tile_parity(t))) return false;
-            tc_fence_after();
-            const uint32_t v = base + W::kOffV + s * W::kKvBytes;
+            const uint32_t v = v_desc + s * (W::kKvBytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kTok / 16; ++kk) {
-                // 32 tokens' probabilities from column 0 (their rests from 16), the other 32's from column 32
-                const uint32_t pr = tmem + 64 * (t & 1) + 32 * (kk >> 1) + 8 * (kk & 1);
-                mma_f16_ta(tmem + W::kTmO, pr, sw128_mn_desc(v + kk * 2048, W::kKvBlock), idesc_o, first && kk == 0 ? 0u : 1u);
-                if constexpr (SPLIT)
-                    mma_f16_ta(tmem + W::kTmO, pr + 16, sw128_mn_desc(v + kk * 2048, W::kKvBlock), idesc_o, 1u);
+            for (int j = 0; j < NB; ++j) {
+                if (!wait_for(p_ready + 16 * j + 8 * (t & 1), tile_parity(t))) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kTok / 16; ++kk) {
+                    // 32 tokens' probabilities from column 0 (their rests from 16), the other 32's from column 32
+                    const uint32_t pr = tmem + 128 * j + 64 * (t & 1) + 32 * (kk >> 1) + 8 * (kk & 1);
+                    mma_ts(tmem + W::kTmO + j * D, pr, v + kk * (2048 >> 4), idesc_o, first && kk == 0 ? 0u : 1u);
+                    if constexpr (SPLIT) mma_ts(tmem + W::kTmO + j * D, pr + 16, v + kk * (2048 >> 4), idesc_o, 1u);
+                }
             }
             mma_commit(o_done + 8 * (t & 1));
             return true;
@@ -680,18 +731,22 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t k = base + W::kOffK + s * W::kKvBytes;
+                const uint32_t k = k_desc + s * (W::kKvBytes >> 4);
 #pragma unroll
-                for (int blk = 0; blk < W::kBlk; ++blk)
+                for (int j = 0; j < NB; ++j) {
+                    const uint32_t q = q_desc + j * (W::kQRows >> 4), d = tmem + 128 * j + 64 * (n & 1);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t kd = sw128_desc(k + blk * W::kKvBlock) + 2 * kk;
-                        mma_bf16(tmem + 64 * (n & 1), sw128_desc(base + blk * W::kQBlock) + 2 * kk, kd, idesc_s,
-                                 (blk | kk) == 0 ? 0u : 1u);
-                        if constexpr (SPLIT)
-                            mma_bf16(tmem + 64 * (n & 1), sw128_desc(base + W::kQBytes + blk * W::kQBlock) + 2 * kk, kd, idesc_s, 1u);
+                    for (int i = 0; i < 4 * W::kBlk; ++i) {  // k-steps of 16 dims: 32 bytes of a row
+                        const uint32_t ko = k + (i >> 2) * (W::kKvBlock >> 4) + 2 * (i & 3);
+                        const uint32_t qo = q + (i >> 2) * (W::kQBlock >> 4) + 2 * (i & 3);
+                        if (i == 0)
+                            mma_ss<true>(d, qo, ko, idesc_s);
+                        else
+                            mma_ss<false>(d, qo, ko, idesc_s);
+                        if constexpr (SPLIT) mma_ss<false>(d, qo + (W::kQBytes >> 4), ko, idesc_s);
                     }
-                mma_commit(s_done + 8 * (n & 1));
+                    mma_commit(s_done + 16 * j + 8 * (n & 1));
+                }
                 if (r > r0 && !second(n - 1, r - 1 == r0)) failed = true;
             }
             if (!failed && !second(n - 1, r1 - 1 == r0)) failed = true;
@@ -714,19 +769,21 @@ __global__ void __launch_bounds__(kWinThreads, Win<D, SPLIT>::kCtas)
 // starts in, a warp for each row.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_window_join_kernel(const __grid_constant__ AttnParams p) {
-    constexpr size_t kSlot = kRows * (D + 2);
+    const size_t unit = p.unit_rows, slot_floats = unit * (D + 2);
     const int lane = threadIdx.x & 31;
     griddep_wait();
     const JoinRecord rec = reinterpret_cast<const JoinRecord*>(p.records)[blockIdx.x];
     if (rec.parts == 0) return;
     WinCursor k{rec.b, rec.block, rec.pair, 0, 0, 0};
     const Unit x = win_unit(p, k);
-    const long long rows = static_cast<long long>(x.n) * p.group - x.col0;
-    const float* base = p.part + static_cast<size_t>(blockIdx.x) * 2 * kSlot;
-    auto slot = [&](int i) -> const float* { return i == 0 ? base + kSlot : base + static_cast<size_t>(i) * 2 * kSlot; };
-    for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < min(rows, static_cast<long long>(kRows)); row += gridDim.y * 8) {
+    const int rows = min(x.n * p.group - x.col0, p.unit_rows);
+    const float* base = p.part + static_cast<size_t>(blockIdx.x) * 2 * slot_floats;
+    auto slot = [&](int i) -> const float* {
+        return base + (i == 0 ? 1 : 2 * static_cast<size_t>(i)) * slot_floats;
+    };
+    for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < rows; row += gridDim.y * 8) {
         float mm = -INFINITY;
-        for (int i = lane; i < rec.parts; i += 32) mm = fmaxf(mm, slot(i)[kRows * D + row]);
+        for (int i = lane; i < rec.parts; i += 32) mm = fmaxf(mm, slot(i)[unit * D + row]);
         for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
         float2 v[D / 64];
 #pragma unroll
@@ -735,9 +792,9 @@ __global__ void __launch_bounds__(256) kv4_window_join_kernel(const __grid_const
 #pragma unroll 4
         for (int i = 0; i < rec.parts; ++i) {
             const float* s = slot(i);
-            const float ms = s[kRows * D + row];
+            const float ms = s[unit * D + row];
             const float f = ms == -INFINITY ? 0.0f : exp2_approx(ms - mm);
-            l += s[kRows * D + kRows + row] * f;
+            l += s[unit * D + unit + row] * f;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 const float2 y = *reinterpret_cast<const float2*>(s + row * D + 64 * c + 2 * lane);
@@ -754,9 +811,11 @@ __global__ void __launch_bounds__(256) kv4_window_join_kernel(const __grid_const
 
 constexpr int kMaxSms = 192;  // the workspace is sized for cards of up to as many
 
-template <int D, bool SPLIT>
-cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
-    using W = Win<D, SPLIT>;
+template <int D, bool SPLIT, int NB>
+cudaError_t launch_one(AttnParams p, cudaStream_t stream) {
+    using W = Win<D, SPLIT, NB>;
+    p.unit_rows = W::kUnitRows;
+    p.col_blocks = static_cast<int>((static_cast<long long>(p.c.T) * p.group + W::kUnitRows - 1) / W::kUnitRows);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -764,16 +823,16 @@ cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
     if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1u)) {
-        e = cudaFuncSetAttribute(kv4_window_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
+        e = cudaFuncSetAttribute(kv4_window_kernel<D, SPLIT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
     }
     static_assert(W::kCtas * (W::kSmem + 1024) <= 233472, "the CTAs of an SM fit its shared memory");
     const int ctas = W::kCtas * std::min(sms, kMaxSms);
-    kv4_window_kernel<D, SPLIT><<<ctas, kWinThreads, W::kSmem, stream>>>(p);
+    kv4_window_kernel<D, SPLIT, NB><<<ctas, W::kThreads, W::kSmem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const long long rows = std::min<long long>(static_cast<long long>(p.c.T) * p.group, kRows);
+    const long long rows = std::min<long long>(static_cast<long long>(p.c.T) * p.group, W::kUnitRows);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, static_cast<unsigned>(std::min<long long>((rows + 7) / 8, 4)));
     cfg.blockDim = dim3(256);
@@ -788,7 +847,12 @@ cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch_dim(const AttnParams& p, cudaStream_t stream) {
-    return p.dtype == DType::kF32 ? launch_one<D, true>(p, stream) : launch_one<D, false>(p, stream);
+    const bool split = p.dtype == DType::kF32;
+    if constexpr (D <= 128) {
+        if (static_cast<long long>(p.c.T) * p.group > kRows)
+            return split ? launch_one<D, true, 2>(p, stream) : launch_one<D, false, 2>(p, stream);
+    }
+    return split ? launch_one<D, true, 1>(p, stream) : launch_one<D, false, 1>(p, stream);
 }
 
 }  // namespace
@@ -798,7 +862,6 @@ size_t kv4_window_workspace_bytes(int head_dim) {
 }
 
 cudaError_t launch_kv4_window(AttnParams p, cudaStream_t stream) {
-    p.col_blocks = static_cast<int>((static_cast<long long>(p.c.T) * p.group + kRows - 1) / kRows);
     p.records = p.part + static_cast<size_t>(2 * kMaxSms) * 2 * kRows * (p.c.head_dim + 2);
     switch (p.c.head_dim) {
         case 64: return launch_dim<64>(p, stream);
