@@ -729,13 +729,15 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
     }
 }
 
+constexpr int kJoinThreads = 512;
+
 // Joins the partial results of the units that several CTAs shared, one column per block.
 template <int D, int NT>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int kCols = 8 * NT;
     constexpr size_t kSlot = kCols * (D + 2);
-    __shared__ float2 sums[128];
-    __shared__ float lsum[128];
+    __shared__ float2 sums[kJoinThreads];
+    __shared__ float lsum[kJoinThreads];
     const int lane = threadIdx.x & 31, c = blockIdx.y;
     griddep_wait();
     const JoinRecord rec = reinterpret_cast<const JoinRecord*>(p.records)[blockIdx.x];
@@ -748,10 +750,11 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ A
     float mm = -INFINITY;
     for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, slot(i)[kCols * D + c]);
     for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-    constexpr int kPairs = D / 2, kWays = 128 / kPairs;
+    constexpr int kPairs = D / 2, kWays = kJoinThreads / kPairs;
     const int pair = threadIdx.x % kPairs, way = threadIdx.x / kPairs;
     float2 v = make_float2(0.0f, 0.0f);
     float l = 0.0f;
+#pragma unroll 8
     for (int i = way; i < parts; i += kWays) {
         const float* s = slot(i);
         const float ms = s[kCols * D + c];
@@ -806,7 +809,7 @@ cudaError_t launch_one(const AttnParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, 8 * NT);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -5,8 +5,8 @@
 // block of 16 values, K and V of the same block one after the other, so that
 // both loads are in flight together; consecutive threads take the blocks of a
 // token and then the next token of the same head, so a warp's codes and scales
-// land in contiguous 256- and 32-byte pieces. Reading: one thread per 16 bytes
-// of output, so every store of a warp is one contiguous 512-byte piece.
+// land in contiguous 256- and 32-byte pieces. Reading: 16 bytes of output
+// per place, so every store of a warp is one contiguous 512-byte piece.
 
 #include "gdn_kv4.cuh"
 
@@ -101,18 +101,32 @@ __device__ __forceinline__ uint32_t e2m1_pair(float a, float b) {
     return r;
 }
 
+// Two quotients x / s as e2m1 codes. fp32 values take the correctly rounded quotient. A 16-bit value's quotient is
+// either exactly half way between two codes or off it by 2^-11 of itself at least (x has 11 significant bits, half way
+// points times s have 7), so the product with 1 / s, within 2^-22 of the quotient, decides as well once it is rounded
+// to 16 bits, which makes a half way point exact again: 5 operations for a pair instead of about 18.
+template <typename T>
+__device__ __forceinline__ uint32_t code_pair(float a, float b, float s, float r) {
+    if constexpr (sizeof(T) == 4) return e2m1_pair(__fdiv_rn(a, s), __fdiv_rn(b, s));
+    const float2 y = __fmul2_rn(make_float2(a, b), make_float2(r, r));
+    const float2 c = __fmul2_rn(y, make_float2(257.0f, 257.0f));  // c - (c - y) is y to 16 bits (Dekker's splitting)
+    const float2 d = __fadd2_rn(c, make_float2(-y.x, -y.y));
+    return e2m1_pair(c.x - d.x, c.y - d.y);
+}
+
 // The block's codes (8 bytes, value 0 in the lowest nibble) and its scale byte.
-// Every step is the correctly rounded operation, so the codes do not depend on
+// The codes are those of the exact quotients, so they do not depend on
 // the order of work: a plain restatement gives the same bytes.
+template <typename T>
 __device__ __forceinline__ uint32_t quantise16(float (&x)[16], uint2& codes) {
     float a = fabsf(x[0]);
 #pragma unroll
     for (int i = 1; i < 16; ++i) a = max_nan(a, fabsf(x[i]));
-    if (a != a) {  // NaN counts as 0
+    if (!(a <= 6.0f * kKv4MaxScale)) {  // NaN counts as 0, what is larger saturates
         a = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            x[i] = x[i] == x[i] ? x[i] : 0.0f;
+            x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -6.0f * kKv4MaxScale), 6.0f * kKv4MaxScale) : 0.0f;
             a = fmaxf(a, fabsf(x[i]));
         }
     }
@@ -121,11 +135,10 @@ __device__ __forceinline__ uint32_t quantise16(float (&x)[16], uint2& codes) {
         codes = make_uint2(0u, 0u);
         return 0u;
     }
-    const float s = scale_value(byte);
+    const float s = scale_value(byte), r = __frcp_rn(s);
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        w[i >> 2] |= e2m1_pair(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s)) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) w[i >> 2] |= code_pair<T>(x[2 * i], x[2 * i + 1], s, r) << (8 * (i & 3));
     codes = make_uint2(w[0], w[1]);
     return byte;
 }
@@ -161,10 +174,10 @@ __global__ void __launch_bounds__(kCacheThreads) kv4_append_kernel(const __grid_
     const int code_at = r * (D / 2) + (blk ^ kv4_swizzle(r, kBlocks)) * 8;
     const int scale_at = psize * (D / 2) + r * kBlocks + blk;
     uint2 codes;
-    uint32_t s = quantise16(k, codes);
+    uint32_t s = quantise16<T>(k, codes);
     *reinterpret_cast<uint2*>(kc + code_at) = codes;
     kc[scale_at] = static_cast<uint8_t>(s);
-    s = quantise16(v, codes);
+    s = quantise16<T>(v, codes);
     *reinterpret_cast<uint2*>(vc + code_at) = codes;
     vc[scale_at] = static_cast<uint8_t>(s);
 }
@@ -204,55 +217,75 @@ __device__ __forceinline__ void store_values(T* out, uint32_t codes, __half2 s) 
     __stcs(reinterpret_cast<uint4*>(out), make_uint4(o[0], o[1], o[2], o[3]));
 }
 
+// kReadItems places per thread, kCacheThreads apart, step by step: what a place needs is found by three
+// dependent loads (the window, the page's number, the codes), and one place per thread spent its life waiting for them.
+constexpr int kReadItems = 4;
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kCacheThreads) kv4_read_kernel(const __grid_constant__ CacheParams p) {
-    constexpr int kPer = 16 / static_cast<int>(sizeof(T));  // values per thread
+    constexpr int kPer = 16 / static_cast<int>(sizeof(T));  // values per place
     constexpr int kChunks = D / kPer;
-    const unsigned long long item = static_cast<unsigned long long>(blockIdx.x) * kCacheThreads + threadIdx.x;
-    const int d = (static_cast<int>(item) & (kChunks - 1)) * kPer;
-    if (item / kChunks >= p.rows) return;
-    const uint32_t row = static_cast<uint32_t>(item / kChunks);  // ((b L + l) T + t) kv_heads + h
-    const uint32_t blt = p.by_heads.div(row);
-    const int h = static_cast<int>(row - blt * p.by_heads.d);
-    const uint32_t bl = p.by_t.div(blt);
-    const int t = static_cast<int>(blt - bl * p.by_t.d);
-    const int b = static_cast<int>(p.by_layers.div(bl));
-    const int l = static_cast<int>(bl - b * p.by_layers.d);
-    const Kv4Window w = kv4_window(p.c, b);
-    if (t >= w.n) return;
-    const int page = t < w.cap - w.start ? kv4_page(p.c, b, w.start + t) : -1;
-    T* ko = static_cast<T*>(p.out_k) + static_cast<size_t>(row) * D + d;
-    T* vo = static_cast<T*>(p.out_v) + static_cast<size_t>(row) * D + d;
-    if (page < 0) {  // a token that is not there reads as zeros
-        if (d == 0) atomicOr(&g_kv4_cache_error, kErrBadPage);
-        store_values(ko, 0u, __float2half2_rn(0.0f));
-        store_values(vo, 0u, __float2half2_rn(0.0f));
-        return;
-    }
     const int psize = 1 << p.c.page_shift;
-    const int r = (w.start + t) & (psize - 1);
-    const uint8_t* kc = p.c.cache + kv4_head_offset(p.c, l, page, h);
-    const uint8_t* vc = kc + kv4_head_bytes(psize, D) / 2;
-    const int code_at = r * (D / 2) + ((d >> 4) ^ kv4_swizzle(r, D / 16)) * 8 + ((d & 15) >> 1);
-    const int scale_at = psize * (D / 2) + r * (D / 16) + (d >> 4);
-    uint32_t kw, vw;
-    if constexpr (kPer == 8) {
-        kw = *reinterpret_cast<const uint32_t*>(kc + code_at);
-        vw = *reinterpret_cast<const uint32_t*>(vc + code_at);
-    } else {
-        kw = *reinterpret_cast<const uint16_t*>(kc + code_at);
-        vw = *reinterpret_cast<const uint16_t*>(vc + code_at);
+    const unsigned long long item0 = static_cast<unsigned long long>(blockIdx.x) * (kCacheThreads * kReadItems) + threadIdx.x;
+    const int d = (static_cast<int>(item0) & (kChunks - 1)) * kPer;  // kCacheThreads is a multiple of kChunks
+    uint32_t row[kReadItems];
+    int h[kReadItems], l[kReadItems], b[kReadItems], t[kReadItems], pos[kReadItems], page[kReadItems];
+    bool on[kReadItems];
+#pragma unroll
+    for (int i = 0; i < kReadItems; ++i) {
+        const unsigned long long r = (item0 + i * kCacheThreads) / kChunks;  // ((b L + l) T + t) kv_heads + h
+        on[i] = r < p.rows;
+        row[i] = on[i] ? static_cast<uint32_t>(r) : 0u;
+        const uint32_t blt = p.by_heads.div(row[i]);
+        h[i] = static_cast<int>(row[i] - blt * p.by_heads.d);
+        const uint32_t bl = p.by_t.div(blt);
+        t[i] = static_cast<int>(blt - bl * p.by_t.d);
+        b[i] = static_cast<int>(p.by_layers.div(bl));
+        l[i] = static_cast<int>(bl - b[i] * p.by_layers.d);
     }
-    const __half2 ks = __half2half2(__ushort_as_half(static_cast<unsigned short>(kc[scale_at] << 7)));
-    const __half2 vs = __half2half2(__ushort_as_half(static_cast<unsigned short>(vc[scale_at] << 7)));
-    store_values(ko, kw, ks);
-    store_values(vo, vw, vs);
+#pragma unroll
+    for (int i = 0; i < kReadItems; ++i) {
+        const Kv4Window w = kv4_window(p.c, b[i]);
+        on[i] = on[i] && t[i] < w.n;
+        pos[i] = t[i] < w.cap - w.start ? w.start + t[i] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kReadItems; ++i) page[i] = on[i] && pos[i] >= 0 ? kv4_page(p.c, b[i], pos[i]) : -1;
+    uint32_t kw[kReadItems], vw[kReadItems], ks[kReadItems], vs[kReadItems];
+#pragma unroll
+    for (int i = 0; i < kReadItems; ++i) {
+        kw[i] = vw[i] = ks[i] = vs[i] = 0u;  // a token that is not there reads as zeros
+        if (page[i] < 0) continue;
+        const int r = pos[i] & (psize - 1);
+        const uint8_t* kc = p.c.cache + kv4_head_offset(p.c, l[i], page[i], h[i]);
+        const uint8_t* vc = kc + kv4_head_bytes(psize, D) / 2;
+        const int code_at = r * (D / 2) + ((d >> 4) ^ kv4_swizzle(r, D / 16)) * 8 + ((d & 15) >> 1);
+        const int scale_at = psize * (D / 2) + r * (D / 16) + (d >> 4);
+        if constexpr (kPer == 8) {
+            kw[i] = *reinterpret_cast<const uint32_t*>(kc + code_at);
+            vw[i] = *reinterpret_cast<const uint32_t*>(vc + code_at);
+        } else {
+            kw[i] = *reinterpret_cast<const uint16_t*>(kc + code_at);
+            vw[i] = *reinterpret_cast<const uint16_t*>(vc + code_at);
+        }
+        ks[i] = kc[scale_at];
+        vs[i] = vc[scale_at];
+    }
+#pragma unroll
+    for (int i = 0; i < kReadItems; ++i) {
+        if (!on[i]) continue;
+        if (page[i] < 0 && d == 0) atomicOr(&g_kv4_cache_error, kErrBadPage);
+        const size_t at = static_cast<size_t>(row[i]) * D + d;
+        store_values(static_cast<T*>(p.out_k) + at, kw[i], __half2half2(__ushort_as_half(static_cast<unsigned short>(ks[i] << 7))));
+        store_values(static_cast<T*>(p.out_v) + at, vw[i], __half2half2(__ushort_as_half(static_cast<unsigned short>(vs[i] << 7))));
+    }
 }
 
 template <typename T, int D>
 cudaError_t launch_one(bool append, const CacheParams& p, cudaStream_t stream) {
     const unsigned long long per_row = append ? D / 16 : D * sizeof(T) / 16;
-    const unsigned long long blocks = (p.rows * per_row + kCacheThreads - 1) / kCacheThreads;
+    const unsigned long long per_block = append ? kCacheThreads : kCacheThreads * kReadItems;
+    const unsigned long long blocks = (p.rows * per_row + per_block - 1) / per_block;
     if (append)
         kv4_append_kernel<T, D><<<static_cast<unsigned>(blocks), kCacheThreads, 0, stream>>>(p);
     else

@@ -407,41 +407,51 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             const int b = cur.b;
             const int rows = min(x.n * p.group - x.col0, kUnitRows);
             if (tid == 32 && x.n > kv4_window(p.c, b).cap - x.start) atomicOr(&g_kv4_window_error, kErrBadPage);
-            // queries of half of these rows, scaled to fill fp16's range
-#pragma unroll 2
-            for (int i = 0; i < 16; ++i) {
-                const int rr = 128 * block + 32 * quarter + 16 * half + i;
-                if (rr >= rows) break;
+            // queries, scaled to fill fp16's range: row 8 i + this warp of the block's eight, kAtOnce rows in flight
+            constexpr int kAtOnce = D > 128 ? 2 : 4;
+            const int mine = 128 * block + ((warp - 1) & 7);
+#pragma unroll 1
+            for (int i0 = 0; i0 < 16; i0 += kAtOnce) {
+                if (mine + 8 * i0 >= rows) break;
                 constexpr int kChunks = D > 128 ? D / 128 : 1;
-                float4 v[kChunks];
-                float a = 0.0f;
+                float4 v[kAtOnce][kChunks];
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    v[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (4 * lane + 128 * c < D) v[c] = load_q4(p, q_row(p, b, x, x.col0 + rr) + 128 * c + 4 * lane);
-                    a = fmaxf(fmaxf(a, fmaxf(fabsf(v[c].x), fabsf(v[c].y))), fmaxf(fabsf(v[c].z), fabsf(v[c].w)));
-                }
+                for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
-                const float f = row_factor(a);
-                if (lane == 0) mul_s[rr] = fmaxf(p.scale_log2 / f, kLeastScale);
+                    for (int c = 0; c < kChunks; ++c) {
+                        const int rr = mine + 8 * (i0 + i);
+                        v[i][c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (rr < rows && 4 * lane + 128 * c < D) v[i][c] = load_q4(p, q_row(p, b, x, x.col0 + rr) + 128 * c + 4 * lane);
+                    }
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    const int d = 4 * lane + 128 * c;
-                    if (d >= D) continue;
-                    const uint32_t at = block * W::kQRows + (d >> 6) * W::kQBlock + sw128_offset(rr & 127, (d & 63) >> 3) + (d & 7) * 2;
-                    const float q0 = v[c].x * f, q1 = v[c].y * f, q2 = v[c].z * f, q3 = v[c].w * f;
-                    const uint2 hi = make_uint2(pack_half2(q0, q1), pack_half2(q2, q3));
-                    *reinterpret_cast<uint2*>(sm + at) = hi;
-                    if constexpr (SPLIT)
-                        *reinterpret_cast<uint2*>(sm + W::kQBytes + at) =
-                            make_uint2(pack_rest(q0, q1, hi.x), pack_rest(q2, q3, hi.y));
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const int rr = mine + 8 * (i0 + i);
+                    float a = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c)
+                        a = fmaxf(fmaxf(a, fmaxf(fabsf(v[i][c].x), fabsf(v[i][c].y))), fmaxf(fabsf(v[i][c].z), fabsf(v[i][c].w)));
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
+                    const float f = row_factor(a);
+                    if (lane == 0) mul_s[rr] = fmaxf(p.scale_log2 / f, kLeastScale);
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        const int d = 4 * lane + 128 * c;
+                        if (d >= D) continue;
+                        const uint32_t at = block * W::kQRows + (d >> 6) * W::kQBlock + sw128_offset(rr & 127, (d & 63) >> 3) + (d & 7) * 2;
+                        const float q0 = v[i][c].x * f, q1 = v[i][c].y * f, q2 = v[i][c].z * f, q3 = v[i][c].w * f;
+                        const uint2 hi = make_uint2(pack_half2(q0, q1), pack_half2(q2, q3));
+                        *reinterpret_cast<uint2*>(sm + at) = hi;
+                        if constexpr (SPLIT)
+                            *reinterpret_cast<uint2*>(sm + W::kQBytes + at) =
+                                make_uint2(pack_rest(q0, q1, hi.x), pack_rest(q2, q3, hi.y));
+                    }
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_local(q_full);
-            (void)exchange(0.0f);  // the other half's rows have their factors
+            asm volatile("bar.sync %0, 256;" ::"r"(1 + 4 * NB + block) : "memory");  // the block's rows have their factors
 
             const bool some = 128 * block + 32 * quarter < rows;  // this warp has rows
             const float mul = row < rows ? mul_s[row] : kLeastScale;
