@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
     }
 }
 
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
 
 // Joins the partial results of the units that several CTAs shared, one column per block.
 template <int D, int NT>
