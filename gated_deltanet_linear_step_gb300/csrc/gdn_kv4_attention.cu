@@ -62,7 +62,7 @@ __device__ unsigned int g_kv4_attn_error = 0;
 // A warp's tile: kTokens tokens of one kv head, K codes | V codes | K scales | V scales.
 template <int D>
 struct Tile {
-    static constexpr int kTokens = D == 64 ? 64 : 32;
+    static constexpr int kTokens = D == 256 ? 32 : 64;
     static constexpr int kRow = D / 2;      // code bytes of a token
     static constexpr int kBlocks = D / 16;  // scales of a token
     static constexpr uint32_t kCodeBytes = kTokens * kRow;
@@ -206,11 +206,14 @@ __device__ __forceinline__ int dim_of(int pos) {
 }
 
 // ---------------------------------------------------------------- kernel --
-// Resident CTAs per SM (a block's registers and shared memory allow them) and tiles in a warp's ring.
+// Resident CTAs per SM, as a block's registers and shared memory allow, and tiles in a warp's ring. 64 sequences of
+// 16384 tokens, 8 heads of 128, one query token: tiles of 32 tokens 223 us (3 CTAs, 3 tiles) and 228 us (4 CTAs,
+// 2 tiles, 128 registers), of 64 tokens 210 us (2 CTAs, 2 tiles) and 204 us (3 CTAs, 2 tiles): the work per tile that
+// does not depend on its length is a third of a 32-token tile's instructions.
 template <int D, int NT, bool SPLIT>
 struct Shape {
-    static constexpr int kCtas = D == 256 ? 2 : NT == 1 ? 3 : 2;
-    static constexpr int kStages = D == 256 ? 2 : NT == 1 ? 3 : 4;
+    static constexpr int kCtas = D <= 128 && NT == 1 && !SPLIT ? 3 : 2;
+    static constexpr int kStages = 2;
 };
 
 template <int D, int NT, bool SPLIT>
