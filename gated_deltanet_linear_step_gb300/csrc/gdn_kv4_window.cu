@@ -45,8 +45,7 @@ namespace gdn {
 namespace {
 
 constexpr int kRows = 128;       // of a block
-constexpr int kTok = 64;         // of a tile
-constexpr int kStartCost = 4;    // places of a block's start on the line, in tiles
+constexpr int kStartTokens = 512;  // a unit's start takes as many places on the line as this many tokens
 
 __device__ unsigned int g_kv4_window_error = 0;
 
@@ -58,6 +57,11 @@ struct Win {
     static constexpr int kUnpackWarps = D == 128 ? 4 * NB : 4;
     static constexpr int kThreads = 32 * (1 + kSoftWarps + kUnpackWarps);
     static constexpr int kUnitRows = NB * kRows;
+    // Tiles of 64 tokens with two buffers of scores, or of 128 tokens, for which the first product runs at twice the rate,
+    // with one (there is no more tensor memory): 2 x 1024 tokens behind 8000, 32 heads, take 328 us with the former and
+    // 354 us with the latter at D = 128, 280 and 257 us at D = 64.
+    static constexpr int kTok = NB == 2 && D == 64 ? 128 : 64;
+    static constexpr int kBuffers = kTok == 128 ? 1 : 2;
     static constexpr int kStages = D == 256 && SPLIT ? 1 : 2;
     static constexpr int kBlk = D / 64;                        // 64-dim blocks of a row (128 bytes)
     static constexpr uint32_t kQBlock = kRows * 128;           // bytes of a block of Q
@@ -71,14 +75,14 @@ struct Win {
     static constexpr uint32_t kOffBad = kOffMul + kUnitRows * 4;     // missing pages of tiles j mod 4
     static constexpr uint32_t kOffXch = kOffBad + 4 * 4;             // what the two halves of a row tell each other
     static constexpr uint32_t kOffBar = kOffXch + 2 * 2 * kUnitRows * 4;
-    static constexpr uint32_t kBars = 2 + 2 + 2 * NB + 2 * NB + 2 + 1 + 1;  // see below
+    static constexpr uint32_t kBars = 2 + 2 + 1 + 1 + 3 * 2 * NB;   // see below
     static constexpr uint32_t kUsed = kOffBar + kBars * 8 + 64;      // + cursor, tensor memory address
     static constexpr int kCtas = NB == 1 && D <= 128 && 2 * (kUsed + 2048) <= 232448 ? 2 : 1;
     // no more CTAs than the tensor memory has room for: a third (second) would wait in its allocation
     static constexpr uint32_t kLeast = kCtas == 2 ? 80 * 1024 : 118 * 1024;
     static constexpr uint32_t kSmem = (kUsed + 1024 > kLeast ? kUsed + 1024 : kLeast);
     static constexpr uint32_t kTmCols = NB * (128 + D) <= 256 ? 256 : 512;
-    static constexpr uint32_t kTmO = NB * 128;                       // scores of block i at 128 i, + 64
+    static constexpr uint32_t kTmO = NB * 128;                       // scores of block i from 128 i, buffers kTok apart
     static_assert(NB * (128 + D) <= 512, "scores and sums fit the tensor memory");
 };
 
@@ -98,7 +102,7 @@ __device__ __forceinline__ int block_end(const AttnParams& p, const Kv4Window& w
 
 __device__ __forceinline__ int block_cost(const AttnParams& p, const Kv4Window& w, int blk) {
     const int end = block_end(p, w, blk);
-    return end == 0 ? 0 : kStartCost + (end + kTok - 1) / kTok;
+    return end == 0 ? 0 : (kStartTokens + end + (1 << p.tile_shift) - 1) >> p.tile_shift;
 }
 
 // Cost of block i % col_blocks of sequence i / col_blocks.
@@ -158,9 +162,10 @@ __device__ __forceinline__ void next_unit(const AttnParams& p, int pairs, WinCur
 }
 
 // The tiles [r0, r1) of the cursor's unit that are its CTA's.
-__device__ __forceinline__ void unit_tiles(const WinCursor& k, int& r0, int& r1) {
-    r0 = max(k.at - kStartCost, 0);
-    r1 = min(k.cost, k.at + k.left) - kStartCost;
+__device__ __forceinline__ void unit_tiles(const AttnParams& p, const WinCursor& k, int& r0, int& r1) {
+    const int start = kStartTokens >> p.tile_shift;
+    r0 = max(k.at - start, 0);
+    r1 = min(k.cost, k.at + k.left) - start;
 }
 
 __device__ __forceinline__ Unit win_unit(const AttnParams& p, const WinCursor& k) {
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
     kv4_window_kernel(const __grid_constant__ AttnParams p) {
     using W = Win<D, SPLIT, NB>;
     constexpr int kStages = W::kStages, kSoftWarps = W::kSoftWarps, kUnpackWarps = W::kUnpackWarps;
-    constexpr int kUnitRows = W::kUnitRows;
+    constexpr int kUnitRows = W::kUnitRows, kTok = W::kTok, kBuffers = W::kBuffers;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
     unsigned char* sm = smem_raw + (base - raw);
@@ -330,9 +335,9 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(cur_s + 1);
     const uint32_t bars = base + W::kOffBar;
     const uint32_t k_full = bars, v_full = bars + 16;      // per stage: unpacked
-    const uint32_t o_done = bars + 32;                     // per parity of the tile
-    const uint32_t q_full = bars + 48, drained = bars + 56;
-    const uint32_t s_done = bars + 64, p_ready = s_done + 16 * NB;  // per block and parity
+    const uint32_t q_full = bars + 32, drained = bars + 40;
+    // per block and parity of the tile
+    const uint32_t s_done = bars + 48, p_ready = s_done + 16 * NB, o_done = p_ready + 16 * NB;
     float* xch = reinterpret_cast<float*>(sm + W::kOffXch);
     const int pairs = p.c.L * p.c.kv_heads;
 
@@ -355,8 +360,8 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
         for (int i = 0; i < 2; ++i) {
             mbar_init(k_full + 8 * i, kUnpackWarps);
             mbar_init(v_full + 8 * i, kUnpackWarps);
-            mbar_init(o_done + 8 * i, 1);
             for (int j = 0; j < NB; ++j) {
+                mbar_init(o_done + 16 * j + 8 * i, 1);
                 mbar_init(s_done + 16 * j + 8 * i, 1);
                 mbar_init(p_ready + 16 * j + 8 * i, 8);
             }
@@ -377,7 +382,8 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
 
-    // Tile n of the CTA (counted over all its units) uses stage n mod kStages of K and V and buffer n mod 2 of the scores.
+    // Tile n of the CTA (counted over all its units) uses stage n mod kStages of K and V and buffer n mod kBuffers of the
+    // scores; barriers per tile alternate by its parity.
     auto stage_parity = [](int n) -> uint32_t { return static_cast<uint32_t>(n / kStages) & 1u; };
     auto tile_parity = [](int n) -> uint32_t { return static_cast<uint32_t>(n >> 1) & 1u; };
     bool failed = false;
@@ -401,7 +407,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
         };
         for (; cur.left > 0; next_unit(p, pairs, cur)) {
             int r0, r1;
-            unit_tiles(cur, r0, r1);
+            unit_tiles(p, cur, r0, r1);
             if (r1 <= r0) break;
             const Unit x = win_unit(p, cur);
             const int b = cur.b;
@@ -462,23 +468,33 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                 if (!failed && !warp_wait(s_done + 16 * block + 8 * (n & 1), tile_parity(n))) failed = true;
                 tc_fence_after();
                 if (some) {
-                    const uint32_t s_at = lanes + 128 * block + 64 * (n & 1) + 32 * half;  // the half's scores, then probabilities
-                    const int p0 = r * kTok + 32 * half;  // this half's first position
-                    const uint32_t bad = bad_s[n & 3] >> (2 * half);
+                    constexpr int kHalf = kTok / 2, kChunks = kHalf / 32;
+                    // the half's scores, then, per 32 of them, 16 columns of probabilities and 16 of their rests
+                    const uint32_t s_at = lanes + 128 * block + kTok * (n % kBuffers) + kHalf * half;
+                    const int p0 = r * kTok + kHalf * half;  // its first position
+                    const uint32_t bad = (bad_s[n & 3] >> (kHalf / 16 * half)) & ((1u << (kHalf / 16)) - 1u);
+                    const bool part = p0 + kHalf > seen_by_all || bad != 0;
                     float s[32];
-                    tmem_read32(s_at, s);
-                    if (p0 + 32 > seen_by_all || bad != 0) {
+                    auto scores = [&](int c) {
+                        tmem_read32(s_at + 32 * c, s);
+                        if (part) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (p0 + i > lim || ((bad >> (i >> 4)) & 1u)) s[i] = -INFINITY;
-                    }
-                    float t0 = max3(s[0], s[1], s[2]), t1 = max3(s[3], s[4], s[5]);
+                            for (int i = 0; i < 32; ++i)
+                                if (p0 + 32 * c + i > lim || ((bad >> (2 * c + (i >> 4))) & 1u)) s[i] = -INFINITY;
+                        }
+                    };
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int i = 6; i < 30; i += 4) {
-                        t0 = max3(t0, s[i], s[i + 1]);
-                        t1 = max3(t1, s[i + 2], s[i + 3]);
+                    for (int c = 0; c < kChunks; ++c) {
+                        scores(c);
+                        float t0 = max3(s[0], s[1], s[2]), t1 = max3(s[3], s[4], s[5]);
+#pragma unroll
+                        for (int i = 6; i < 30; i += 4) {
+                            t0 = max3(t0, s[i], s[i + 1]);
+                            t1 = max3(t1, s[i + 2], s[i + 3]);
+                        }
+                        top = max3(top, max3(t0, s[30], s[31]), t1);
                     }
-                    float top = fmaxf(max3(t0, s[30], s[31]), t1);
                     top = fmaxf(top, exchange(top));
                     if (__any_sync(~0u, fmaf(top, mul, shift) > kPShift + kSlack)) {
                         const float v = fmaxf(m, top * mul);
@@ -487,7 +503,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                         shift = v == -INFINITY ? kNone : kPShift - v;
                         l *= al;
                         if (r > r0) {  // this half of the sums so far: after the product that is adding to them
-                            if (!failed && !warp_wait(o_done + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
+                            if (!failed && !warp_wait(o_done + 16 * block + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
                             tc_fence_after();
 #pragma unroll 1
                             for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
@@ -501,22 +517,26 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                     }
                     float2 sum = make_float2(0.0f, 0.0f);
                     const float2 mul2 = make_float2(mul, mul), shift2 = make_float2(shift, shift);
-                    uint32_t hi[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), mul2, shift2);
-                        s[2 * i] = exp2_approx(e.x);
-                        s[2 * i + 1] = exp2_approx(e.y);
-                        sum = __fadd2_rn(sum, make_float2(s[2 * i], s[2 * i + 1]));
-                        hi[i] = pack_half2(s[2 * i], s[2 * i + 1]);
+                    for (int c = kChunks - 1; c >= 0; --c) {  // the last chunk is still in registers
+                        if (c < kChunks - 1) scores(c);
+                        uint32_t hi[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), mul2, shift2);
+                            s[2 * i] = exp2_approx(e.x);
+                            s[2 * i + 1] = exp2_approx(e.y);
+                            sum = __fadd2_rn(sum, make_float2(s[2 * i], s[2 * i + 1]));
+                            hi[i] = pack_half2(s[2 * i], s[2 * i + 1]);
+                        }
+                        tmem_st16(s_at + 32 * c, hi);
+                        if constexpr (SPLIT) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) hi[i] = pack_rest(s[2 * i], s[2 * i + 1], hi[i]);
+                            tmem_st16(s_at + 32 * c + 16, hi);
+                        }
                     }
                     l += sum.x + sum.y;
-                    tmem_st16(s_at, hi);
-                    if constexpr (SPLIT) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) hi[i] = pack_rest(s[2 * i], s[2 * i + 1], hi[i]);
-                        tmem_st16(s_at + 16, hi);
-                    }
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -526,9 +546,9 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             // outputs: each half its dims
             const float other = exchange(l);
             l = half == 0 ? l + other : other + l;
-            if (!failed && !warp_wait(o_done + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
+            if (!failed && !warp_wait(o_done + 16 * block + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
             tc_fence_after();
-            const bool done = r0 == 0 && r1 == cur.cost - kStartCost;
+            const bool done = r0 == 0 && r1 == cur.cost - (kStartTokens >> p.tile_shift);
             if (some) {
                 float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kUnitRows * (D + 2));
                 const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // no key at all: zeros
@@ -564,10 +584,11 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
     } else if (warp > kSoftWarps) {
         // ---------------------------------------------------------------- unpack
         constexpr int kChunksPerRow = D / 32;            // 16 bytes of codes: 32 dims, two scales
-        constexpr int kMine = 2 * kChunksPerRow / kUnpackWarps;  // chunks of K (and of V) per thread
+        constexpr int kMine = kTok * kChunksPerRow / (32 * kUnpackWarps);  // chunks of K (and of V) per thread
         const int uw = warp - 1 - kSoftWarps;
         const int psize = 1 << p.c.page_shift;
-        const int shift = min(p.c.page_shift, 6);
+        constexpr int kTokShift = kTok == 128 ? 7 : 6;
+        const int shift = min(p.c.page_shift, kTokShift);
         const uint32_t head_bytes = static_cast<uint32_t>(kv4_head_bytes(psize, D)), page_bytes = head_bytes * p.c.kv_heads;
         // a thread's chunks are the same place of rows kStep apart
         constexpr int kStep = 8 * (4 * kUnpackWarps / kChunksPerRow);
@@ -593,7 +614,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                     return;
                 }
                 int r0, r1;
-                unit_tiles(ahead, r0, r1);
+                unit_tiles(p, ahead, r0, r1);
                 const Unit x = win_unit(p, ahead);
                 a_r = r0;
                 a_r1 = r1;
@@ -611,10 +632,10 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
         uint32_t bad = 0;
         auto fetch = [&]() {
             const int p0 = a_r * kTok;
-            if (shift == 6 && p0 + kTok <= a_end) {  // a whole tile of one page
+            if (shift == kTokShift && p0 + kTok <= a_end) {  // a whole tile of one page
                 int page = __ldg(a_table + (p0 >> p.c.page_shift));
                 if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.n_pages)) page = -1;
-                bad = page < 0 ? 15u : 0u;
+                bad = page < 0 ? (1u << (kTok / 16)) - 1u : 0u;
                 const int in_page = p0 & (psize - 1);
                 const uint8_t* k = a_head + static_cast<unsigned long long>(static_cast<uint32_t>(max(page, 0))) * page_bytes;
                 const uint8_t* v = k + head_bytes / 2;
@@ -629,7 +650,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                 }
                 return;
             }
-            // lane j < 4 looks up page j of the tile
+            // lane j looks up page j of the tile
             const int pos = p0 + (lane << shift);
             const bool want = lane < (kTok >> shift) && pos < a_end;
             int page = want ? __ldg(a_table + (pos >> p.c.page_shift)) : 0;
@@ -638,7 +659,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             // the missing pages as 16-token groups, whatever the page size
             bad = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) bad |= ((gone >> ((16 * q) >> shift)) & 1u) << q;
+            for (int q = 0; q < kTok / 16; ++q) bad |= ((gone >> ((16 * q) >> shift)) & 1u) << q;
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
                 const int row = row0 + i * kStep, j = row >> shift;
@@ -685,7 +706,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_local(k_full + 8 * s);
-            if (n >= kStages && !warp_wait(o_done + 8 * ((n - kStages) & 1), tile_parity(n - kStages))) {
+            if (n >= kStages && !warp_wait(o_done + 16 * (NB - 1) + 8 * ((n - kStages) & 1), tile_parity(n - kStages))) {
                 failed = true;
                 break;
             }
@@ -696,36 +717,62 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             if (lane == 0) mbar_arrive_local(v_full + 8 * s);
             ++n;
             step();
-            if (more) fetch();
+            if (more) {
+                fetch();
+            }
         }
     } else if (elect_one()) {
         // -------------------------------------------------------------- products
         const uint32_t idesc_s = idesc_f16(kTok), idesc_o = idesc_f16(D) | kIdescBMnMajor;
         const uint32_t q_desc = desc_k(base), k_desc = desc_k(base + W::kOffK), v_desc = desc_mn(base + W::kOffV, W::kKvBlock);
         int units = 0;
-        // O += P V of tile t
-        auto second = [&](int t, bool first) -> bool {
-            const int s = t % kStages;
-            if (!wait_for(v_full + 8 * s, stage_parity(t))) return false;
-            const uint32_t v = v_desc + s * (W::kKvBytes >> 4);
+        // S = Q K of block j, tile t
+        auto first = [&](int j, int t) {
+            const uint32_t k = k_desc + (t % kStages) * (W::kKvBytes >> 4);
+            const uint32_t q = q_desc + j * (W::kQRows >> 4), d = tmem + 128 * j + kTok * (t % kBuffers);
+            // k-steps of 16 dims, 32 bytes of a row. The rests come first: the tensor cores cut each sum off at fp32, and
+            // so half of the cuts are of small numbers (error of fp32 outputs 1.7e-6 -> 1.25e-6 at 4096 tokens).
+            if constexpr (SPLIT) {
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                if (!wait_for(p_ready + 16 * j + 8 * (t & 1), tile_parity(t))) return false;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < kTok / 16; ++kk) {
-                    // 32 tokens' probabilities from column 0 (their rests from 16), the other 32's from column 32
-                    const uint32_t pr = tmem + 128 * j + 64 * (t & 1) + 32 * (kk >> 1) + 8 * (kk & 1);
-                    mma_ts(tmem + W::kTmO + j * D, pr, v + kk * (2048 >> 4), idesc_o, first && kk == 0 ? 0u : 1u);
-                    if constexpr (SPLIT) mma_ts(tmem + W::kTmO + j * D, pr + 16, v + kk * (2048 >> 4), idesc_o, 1u);
+                for (int i = 0; i < 4 * W::kBlk; ++i) {
+                    const uint32_t ko = k + (i >> 2) * (W::kKvBlock >> 4) + 2 * (i & 3);
+                    const uint32_t qo = q + (W::kQBytes >> 4) + (i >> 2) * (W::kQBlock >> 4) + 2 * (i & 3);
+                    if (i == 0)
+                        mma_ss<true>(d, qo, ko, idesc_s);
+                    else
+                        mma_ss<false>(d, qo, ko, idesc_s);
                 }
             }
-            mma_commit(o_done + 8 * (t & 1));
+#pragma unroll
+            for (int i = 0; i < 4 * W::kBlk; ++i) {
+                const uint32_t ko = k + (i >> 2) * (W::kKvBlock >> 4) + 2 * (i & 3);
+                const uint32_t qo = q + (i >> 2) * (W::kQBlock >> 4) + 2 * (i & 3);
+                if (i == 0 && !SPLIT)
+                    mma_ss<true>(d, qo, ko, idesc_s);
+                else
+                    mma_ss<false>(d, qo, ko, idesc_s);
+            }
+            mma_commit(s_done + 16 * j + 8 * (t & 1));
+        };
+        // O += P V of block j, tile t, once its probabilities are there
+        auto second = [&](int j, int t, bool start) -> bool {
+            if (j == 0 && !wait_for(v_full + 8 * (t % kStages), stage_parity(t))) return false;
+            if (!wait_for(p_ready + 16 * j + 8 * (t & 1), tile_parity(t))) return false;
+            tc_fence_after();
+            const uint32_t v = v_desc + (t % kStages) * (W::kKvBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kTok / 16; ++kk) {
+                // 32 tokens' probabilities from the first of their 32 columns, their rests from the 16th
+                const uint32_t pr = tmem + 128 * j + kTok * (t % kBuffers) + 32 * (kk >> 1) + 8 * (kk & 1);
+                mma_ts(tmem + W::kTmO + j * D, pr, v + kk * (2048 >> 4), idesc_o, start && kk == 0 ? 0u : 1u);
+                if constexpr (SPLIT) mma_ts(tmem + W::kTmO + j * D, pr + 16, v + kk * (2048 >> 4), idesc_o, 1u);
+            }
+            mma_commit(o_done + 16 * j + 8 * (t & 1));
             return true;
         };
         for (; cur.left > 0 && !failed; next_unit(p, pairs, cur)) {
             int r0, r1;
-            unit_tiles(cur, r0, r1);
+            unit_tiles(p, cur, r0, r1);
             if (r1 <= r0) break;
             if (!wait_for(q_full, static_cast<uint32_t>(units) & 1u)) {
                 failed = true;
@@ -733,45 +780,36 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             }
             ++units;
             for (int r = r0; r < r1 && !failed; ++r, ++n) {
-                const int s = n % kStages;
-                // (the buffer's last reader, the second product of tile n - 2, has completed)
-                if (!wait_for(k_full + 8 * s, stage_parity(n)) ||
-                    (n >= 2 && !wait_for(o_done + 8 * (n & 1), tile_parity(n - 2)))) {
+                if (!wait_for(k_full + 8 * (n % kStages), stage_parity(n))) {
                     failed = true;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t k = k_desc + s * (W::kKvBytes >> 4);
-#pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    const uint32_t q = q_desc + j * (W::kQRows >> 4), d = tmem + 128 * j + 64 * (n & 1);
-                    // k-steps of 16 dims, 32 bytes of a row. The rests come first: the tensor cores cut each sum off at fp32, and
-                    // so 8 of the 16 cuts are of small numbers (error of fp32 outputs 1.7e-6 -> 1.25e-6 at 4096 tokens).
-                    if constexpr (SPLIT) {
-#pragma unroll
-                        for (int i = 0; i < 4 * W::kBlk; ++i) {
-                            const uint32_t ko = k + (i >> 2) * (W::kKvBlock >> 4) + 2 * (i & 3);
-                            const uint32_t qo = q + (W::kQBytes >> 4) + (i >> 2) * (W::kQBlock >> 4) + 2 * (i & 3);
-                            if (i == 0)
-                                mma_ss<true>(d, qo, ko, idesc_s);
-                            else
-                                mma_ss<false>(d, qo, ko, idesc_s);
+                if constexpr (kBuffers == 2) {  // the next tile's scores before this one's product with V
+                    for (int j = 0; j < NB && !failed; ++j) {
+                        // (the buffer's last reader, the second product of tile n - 2, has completed)
+                        if (n >= 2 && !wait_for(o_done + 16 * j + 8 * (n & 1), tile_parity(n - 2))) {
+                            failed = true;
+                            break;
                         }
+                        tc_fence_after();
+                        first(j, n);
                     }
-#pragma unroll
-                    for (int i = 0; i < 4 * W::kBlk; ++i) {
-                        const uint32_t ko = k + (i >> 2) * (W::kKvBlock >> 4) + 2 * (i & 3);
-                        const uint32_t qo = q + (i >> 2) * (W::kQBlock >> 4) + 2 * (i & 3);
-                        if (i == 0 && !SPLIT)
-                            mma_ss<true>(d, qo, ko, idesc_s);
-                        else
-                            mma_ss<false>(d, qo, ko, idesc_s);
+                    for (int j = 0; j < NB && !failed; ++j)
+                        if (r > r0 && !second(j, n - 1, r - 1 == r0)) failed = true;
+                } else {  // a block's product with V, then its next scores, while the other block's softmax runs
+                    for (int j = 0; j < NB && !failed; ++j) {
+                        if ((r > r0 && !second(j, n - 1, r - 1 == r0)) ||
+                            (n >= 1 && !wait_for(o_done + 16 * j + 8 * ((n - 1) & 1), tile_parity(n - 1)))) {
+                            failed = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        first(j, n);
                     }
-                    mma_commit(s_done + 16 * j + 8 * (n & 1));
                 }
-                if (r > r0 && !second(n - 1, r - 1 == r0)) failed = true;
             }
-            if (!failed && !second(n - 1, r1 - 1 == r0)) failed = true;
+            for (int j = 0; j < NB && !failed; ++j)
+                if (!second(j, n - 1, r1 - 1 == r0)) failed = true;
         }
         // whatever was issued has completed before the tensor memory is freed
         mma_commit(drained);
@@ -837,6 +875,7 @@ template <int D, bool SPLIT, int NB>
 cudaError_t launch_one(AttnParams p, cudaStream_t stream) {
     using W = Win<D, SPLIT, NB>;
     p.unit_rows = W::kUnitRows;
+    p.tile_shift = W::kTok == 128 ? 7 : 6;
     p.col_blocks = static_cast<int>((static_cast<long long>(p.c.T) * p.group + W::kUnitRows - 1) / W::kUnitRows);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
