@@ -8,9 +8,8 @@
 //   s = RNE(min(max|x| / 6, 10240)) to that grid,  code = RNE(x / s) to e2m1.
 // A product of a code and a scale has at most 6 significant bits, is a multiple
 // of 2^-18 and at most 61440: fp16, bf16 and fp32 all hold it exactly, so reading
-// the cache never rounds. An fp16 scale's exponent range is why no per-tensor scale is
-// needed beside it; the price is one mantissa bit less than a signed byte could
-// not have given either (its sign would be unused).
+// the cache never rounds. The exponent range of fp16 is why no per-tensor scale is
+// needed beside the blocks'.
 //
 // Page. For each kv head P tokens: [K codes P x D/2 | K scales P x D/16 |
 // V codes P x D/2 | V scales P x D/16]. The 8-byte code block i of token row r

