@@ -85,7 +85,17 @@ struct Win {
     static constexpr uint32_t kOffXch = kOffBad + 4 * 4;             // what the two halves of a row tell each other
     static constexpr uint32_t kOffBar = kOffXch + 2 * 2 * kUnitRows * 4;
     static constexpr uint32_t kBars = 2 + 2 + 1 + 1 + 3 * 2 * NB;   // see below
-    static constexpr uint32_t kUsed = kOffBar + kBars * 8 + 64;      // + cursor, tensor memory address
+    static constexpr uint32_t kOffSum = kOffBar + kBars * 8 + 64;    // + cursor, tensor memory address
+    // Sums in tensor memory start afresh every 512 tokens (16-bit calls: 16384) and are added up with fp32
+    // instructions, in shared memory where it has room ([dim][row]), otherwise in the CTA's place of the workspace
+    // ([row][dim]): the tensor cores cut off a running sum at every step instead of rounding it, so the error grows
+    // with the steps. fp32, equal values at 16000 tokens: 1.7e-4 without, 7e-6 with. 16 random windows of 8 tokens
+    // after up to 4096: 2.3e-6 without, 1.6e-6 at every 1024, 1.0e-6 here (an fp32 softmax over the unpacked cache
+    // has 1.1e-6), time 48 -> 50 us; 1024 tokens after 8000, two sequences with 32 heads: 680 us at every 1024, 865 us
+    // here. 16-bit calls round their probabilities to 2^-12; at every 16384 the sums lose less, and it costs nothing.
+    static constexpr int kFreshTiles = SPLIT ? 512 / kTok : 16384 / kTok;
+    static constexpr bool kSumInSmem = SPLIT && NB == 1 && D <= 128;
+    static constexpr uint32_t kUsed = kOffSum + (kSumInSmem ? kRows * D * 4 : 0);
     static constexpr int kCtas = NB == 1 && D <= 128 && 2 * (kUsed + 2048) <= 232448 ? 2 : 1;
     // no more CTAs than the tensor memory has room for: a third (second) would wait in its allocation
     static constexpr uint32_t kLeast = kCtas == 2 ? 80 * 1024 : 118 * 1024;
@@ -473,9 +483,61 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             const int lim = row < rows ? min(x.start + (x.col0 + row) / p.group, x.end - 1) : -1;
             const int seen_by_all = min(x.start + x.col0 / p.group + 1, x.end);
             float m = -INFINITY, shift = kNone, l = 0.0f;
+            float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kUnitRows * (D + 2));
+            // sums of earlier tiles, relative to sum_m
+            float* sums = W::kSumInSmem ? reinterpret_cast<float*>(sm + W::kOffSum) + row : slot + row * D;
+            // sixteen of them from dim c on
+            auto get_sums = [&](int c, float* y) {
+                if constexpr (W::kSumInSmem) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] = sums[(c + i) * kRows];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<float4*>(y + i) = *reinterpret_cast<const float4*>(sums + c + i);
+                }
+            };
+            float sum_m = -INFINITY;
+            bool has_sums = false;
+            // the factor of those sums now
+            auto sums_factor = [&]() -> float { return sum_m == -INFINITY ? 0.0f : exp2_approx(sum_m - m); };
             for (int r = r0; r < r1; ++r, ++n) {
                 if (!failed && !warp_wait(s_done + 16 * block + 8 * (n & 1), tile_parity(n))) failed = true;
                 tc_fence_after();
+                const bool fresh = (r - r0) % W::kFreshTiles == 0;  // the sums in tensor memory start with this tile
+                if (some && fresh && r > r0) {
+                    if (!failed && !warp_wait(o_done + 16 * block + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
+                    tc_fence_after();
+                    const float f = sums_factor();
+#pragma unroll 1
+                    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                        uint32_t w[16];
+                        __syncwarp();
+                        tmem_read16(o_at + c, w);
+                        if (row < rows) {
+                            alignas(16) float y[16];
+                            if (has_sums) {
+                                get_sums(c, y);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) y[i] = fmaf(y[i], f, __uint_as_float(w[i]));
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(w[i]);
+                            }
+                            if constexpr (W::kSumInSmem) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) sums[(c + i) * kRows] = y[i];
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4)
+                                    *reinterpret_cast<float4*>(sums + c + i) = *reinterpret_cast<const float4*>(y + i);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    sum_m = m;
+                    has_sums = true;
+                }
                 if (some) {
                     constexpr int kHalf = kTok / 2, kChunks = kHalf / 32;
                     // the half's scores, then, per 32 of them, 16 columns of probabilities and 16 of their rests
@@ -511,7 +573,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                         m = v;
                         shift = v == -INFINITY ? kNone : kPShift - v;
                         l *= al;
-                        if (r > r0) {  // this half of the sums so far: after the product that is adding to them
+                        if (!fresh) {  // this half of the sums so far: after the product that is adding to them
                             if (!failed && !warp_wait(o_done + 16 * block + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
                             tc_fence_after();
 #pragma unroll 1
@@ -559,7 +621,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             tc_fence_after();
             const bool done = r0 == 0 && r1 == cur.cost - (kStartTokens >> p.tile_shift);
             if (some) {
-                float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kUnitRows * (D + 2));
+                const float f = sums_factor();
                 const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // no key at all: zeros
                 const size_t out = row < rows ? q_row(p, b, x, x.col0 + row) : 0;
 #pragma unroll 1
@@ -570,6 +632,12 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                     float o[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(w[i]);
+                    if (has_sums && row < rows) {
+                        alignas(16) float y[16];
+                        get_sums(c, y);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = fmaf(y[i], f, o[i]);
+                    }
                     if (row < rows && done) {
                         store_out16(p, out + c, o, inv);
                     } else if (row < rows) {
@@ -804,10 +872,10 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                         first(j, n);
                     }
                     for (int j = 0; j < NB && !failed; ++j)
-                        if (r > r0 && !second(j, n - 1, r - 1 == r0)) failed = true;
+                        if (r > r0 && !second(j, n - 1, (r - 1 - r0) % W::kFreshTiles == 0)) failed = true;
                 } else {  // a block's product with V, then its next scores, while the other block's softmax runs
                     for (int j = 0; j < NB && !failed; ++j) {
-                        if ((r > r0 && !second(j, n - 1, r - 1 == r0)) ||
+                        if ((r > r0 && !second(j, n - 1, (r - 1 - r0) % W::kFreshTiles == 0)) ||
                             (n >= 1 && !wait_for(o_done + 16 * j + 8 * ((n - 1) & 1), tile_parity(n - 1)))) {
                             failed = true;
                             break;
@@ -818,7 +886,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                 }
             }
             for (int j = 0; j < NB && !failed; ++j)
-                if (!second(j, n - 1, r1 - 1 == r0)) failed = true;
+                if (!second(j, n - 1, (r1 - 1 - r0) % W::kFreshTiles == 0)) failed = true;
         }
         // whatever was issued has completed before the tensor memory is freed
         mma_commit(drained);

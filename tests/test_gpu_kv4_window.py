@@ -133,3 +133,22 @@ def test_graph_replays_as_lengths_advance(cuda_device):
         d.append(k, v, now)
         assert torch.equal(out, d.attend(q, now)), i
     assert g.gdn_read_device_error() == 0
+
+
+@pytest.mark.parametrize("T,D", [(20, 64), (150, 64), (20, 128)])
+def test_long_fp32_sums_are_not_cut_off(cuda_device, T, D):
+    """Values that are all alike: every output is that value (one, as the cache holds it), up to what the fp32 sums over 16000 keys lose. Matrix
+    instructions cut a sum off, by up to 2^-23 of it each: 64 of them before the sums start afresh (512 keys, 16 at
+    a time, probabilities in two parts). Then 32 such sums, rounded; and as many roundings in each partial sum of
+    the probabilities as it has tiles, 250, of either sign (four standard deviations). Enough heads that no
+    sequence is split."""
+    heads, keys = 320, 16000
+    c = Cache(cuda_device, 1, 1, heads, D, 64, keys)
+    k = values((1, 1, keys, 1, D), "bf16", cuda_device, 21).expand(1, 1, keys, heads, D).contiguous()
+    c.append(k, torch.ones_like(k), [0])
+    q = values((1, 1, T, heads, D), "fp32", cuda_device, 22)
+    out = c.attend(q, [keys - T]).double()
+    one = O.kv4_dequantise(*O.kv4_quantise(np.ones(D)))[0]
+    error = (out / float(one) - 1).abs().max().item()
+    print("largest error %.2e" % error)
+    assert error <= 64 * 2**-23 + 32 * 2**-24 + 4 * (32 + 250) ** 0.5 * 2**-24 + 2**-22
