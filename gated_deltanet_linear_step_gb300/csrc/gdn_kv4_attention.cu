@@ -647,9 +647,18 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16(o[4 * wi + i][nt], e01[i], o01[i], e23[i], o23[i], ph[mt][nt][0], ph[mt][nt][1]);
-                            if constexpr (SPLIT)
-                                mma_f16(o[4 * wi + i][nt], e01[i], o01[i], e23[i], o23[i], pl[mt][nt][0], pl[mt][nt][1]);
+                            if constexpr (SPLIT) {
+                                // The tensor cores cut a running sum off at every step, so fp32 calls add each step's
+                                // products to it with fp32 instructions: 4.3e-5 -> 1.7e-6 at 16000 equal values, 49 -> 52 us
+                                // for single tokens of 64 sequences of up to 8192 tokens with 20 heads.
+                                float step[4] = {};
+                                mma_f16(step, e01[i], o01[i], e23[i], o23[i], pl[mt][nt][0], pl[mt][nt][1]);
+                                mma_f16(step, e01[i], o01[i], e23[i], o23[i], ph[mt][nt][0], ph[mt][nt][1]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) o[4 * wi + i][nt][j] += step[j];
+                            } else {
+                                mma_f16(o[4 * wi + i][nt], e01[i], o01[i], e23[i], o23[i], ph[mt][nt][0], ph[mt][nt][1]);
+                            }
                         }
                 }
             }

@@ -135,7 +135,7 @@ def test_graph_replays_as_lengths_advance(cuda_device):
     assert g.gdn_read_device_error() == 0
 
 
-@pytest.mark.parametrize("T,D", [(20, 64), (150, 64), (20, 128)])
+@pytest.mark.parametrize("T,D", [(20, 64), (150, 64), (20, 128), (8, 64), (8, 128)])
 def test_long_fp32_sums_are_not_cut_off(cuda_device, T, D):
     """Values that are all alike: every output is that value (one, as the cache holds it), up to what the fp32 sums over 16000 keys lose. Matrix
     instructions cut a sum off, by up to 2^-23 of it each: 64 of them before the sums start afresh (512 keys, 16 at
