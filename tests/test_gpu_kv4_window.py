@@ -152,3 +152,23 @@ def test_long_fp32_sums_are_not_cut_off(cuda_device, T, D):
     error = (out / float(one) - 1).abs().max().item()
     print("largest error %.2e" % error)
     assert error <= 64 * 2**-23 + 32 * 2**-24 + 4 * (32 + 250) ** 0.5 * 2**-24 + 2**-22
+
+
+@pytest.mark.parametrize("dtype,T,D", [("fp16", 20, 64), ("bf16", 150, 64), ("fp16", 150, 128)])
+def test_long_16_bit_sums(cuda_device, dtype, T, D):
+    """The same for 16-bit calls over 40000 keys, with another value in each dimension: the output's rounding (or half
+    the type's smallest step), the probabilities' (2^-12), 1024 steps before the sums start afresh, and what adds up
+    two more such sums and 625 tiles' probabilities."""
+    heads, keys = 320, 40000
+    c = Cache(cuda_device, 1, 1, heads, D, 64, keys)
+    k = values((1, 1, keys, 1, D), dtype, cuda_device, 23).expand(1, 1, keys, heads, D).contiguous()
+    v = values((D,), dtype, cuda_device, 24)
+    c.append(k, v.expand(k.shape).contiguous(), [0])
+    q = values((1, 1, T, heads, D), dtype, cuda_device, 25)
+    out = c.attend(q, [keys - T]).double()
+    want = torch.from_numpy(O.kv4_dequantise(*O.kv4_quantise(host(v)))).to(cuda_device)
+    info = torch.finfo(TYPES[dtype])
+    tolerance = info.eps / 2 + 2**-12 + 1024 * 2**-23 + 3 * 2**-24 + 4 * 625 ** 0.5 * 2**-24
+    error = (out - want).abs()
+    print("largest error %.2e" % (error / want.abs()).nan_to_num().max().item())
+    assert (error <= tolerance * want.abs() + info.smallest_normal * info.eps / 2).all()
