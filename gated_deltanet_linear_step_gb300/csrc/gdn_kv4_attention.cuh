@@ -24,6 +24,7 @@ struct AttnParams {
     float* part;    // per CTA two partial results: [columns][D] sums, then maxima and sums of the columns
     void* records;  // per CTA a JoinRecord
     int q_heads, group, col_blocks;
+    float* sums;    // of the window kernel: per CTA the sums of earlier tiles
     int unit_rows, tile_shift;  // of the window kernel: rows of a unit, log2 of a tile's tokens
     DType dtype;
     float scale_log2;

@@ -59,7 +59,9 @@ constexpr int kStartTokens = 512;
 __device__ unsigned int g_kv4_window_error = 0;
 
 // NB blocks of 128 rows per CTA share the unpacked tiles: two where a window has as many rows and the tensor memory
-// has room for their sums (D <= 128), one CTA per SM then; otherwise one, and two CTAs per SM where they fit.
+// has room for their sums (D <= 128), one CTA per SM then; otherwise one, and two CTAs per SM where they fit. fp32 calls
+// always take one block, whose sums fit shared memory: 1024 tokens after 8000, two sequences with 32 heads, 559 us (D =
+// 128) and 449 us (D = 64), with two 605 and 469 us.
 template <int D, bool SPLIT, int NB>
 struct Win {
     static constexpr int kSoftWarps = 8 * NB;
@@ -86,16 +88,17 @@ struct Win {
     static constexpr uint32_t kOffBar = kOffXch + 2 * 2 * kUnitRows * 4;
     static constexpr uint32_t kBars = 2 + 2 + 1 + 1 + 3 * 2 * NB;   // see below
     static constexpr uint32_t kOffSum = kOffBar + kBars * 8 + 64;    // + cursor, tensor memory address
-    // Sums in tensor memory start afresh every 512 tokens (16-bit calls: 16384) and are added up with fp32
-    // instructions, in shared memory where it has room ([dim][row]), otherwise in the CTA's place of the workspace
-    // ([row][dim]): the tensor cores cut off a running sum at every step instead of rounding it, so the error grows
-    // with the steps. fp32, equal values at 16000 tokens: 1.7e-4 without, 7e-6 with. 16 random windows of 8 tokens
-    // after up to 4096: 2.3e-6 without, 1.6e-6 at every 1024, 1.0e-6 here (an fp32 softmax over the unpacked cache
-    // has 1.1e-6), time 48 -> 50 us; 1024 tokens after 8000, two sequences with 32 heads: 680 us at every 1024, 865 us
-    // here. 16-bit calls round their probabilities to 2^-12; at every 16384 the sums lose less, and it costs nothing.
+    // Sums in tensor memory start afresh every 512 tokens (16-bit calls: 16384) and are added up with fp32 instructions,
+    // in shared memory where it has room, otherwise in the workspace ([dim / 4][row][4], which a warp reads in whole
+    // lines): the tensor cores cut off a running sum at every step instead of rounding it, so the error grows with the
+    // steps. fp32, equal values at 16000 tokens: 1.7e-4 without, 7e-6 with. 16 random windows of 8 tokens after up to
+    // 4096: 2.3e-6 without, 1.6e-6 at every 1024, 1.0e-6 here (an fp32 softmax over the unpacked cache has 1.1e-6), time
+    // 47.5 -> 48 us; D = 256, two sequences of 1024 tokens after 8000 with 16 heads: 764 -> 826 us. 16-bit calls round
+    // their probabilities to 2^-12; at every 16384 the sums lose less, and it costs nothing.
     static constexpr int kFreshTiles = SPLIT ? 512 / kTok : 16384 / kTok;
-    static constexpr bool kSumInSmem = SPLIT && NB == 1 && D <= 128;
-    static constexpr uint32_t kUsed = kOffSum + (kSumInSmem ? kRows * D * 4 : 0);
+    static constexpr bool kSumInSmem = SPLIT && D <= 128;
+    static_assert(!kSumInSmem || kOffSum % 16 == 0, "read by fours");
+    static constexpr uint32_t kUsed = kOffSum + (kSumInSmem ? kUnitRows * D * 4 : 0);
     static constexpr int kCtas = NB == 1 && D <= 128 && 2 * (kUsed + 2048) <= 232448 ? 2 : 1;
     // no more CTAs than the tensor memory has room for: a third (second) would wait in its allocation
     static constexpr uint32_t kLeast = kCtas == 2 ? 80 * 1024 : 118 * 1024;
@@ -485,17 +488,10 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             float m = -INFINITY, shift = kNone, l = 0.0f;
             float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kUnitRows * (D + 2));
             // sums of earlier tiles, relative to sum_m
-            float* sums = W::kSumInSmem ? reinterpret_cast<float*>(sm + W::kOffSum) + row : slot + row * D;
-            // sixteen of them from dim c on
-            auto get_sums = [&](int c, float* y) {
-                if constexpr (W::kSumInSmem) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = sums[(c + i) * kRows];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        *reinterpret_cast<float4*>(y + i) = *reinterpret_cast<const float4*>(sums + c + i);
-                }
+            auto four_sums = [&](int c) -> float4& {  // of dims c .. c + 3
+                float* sums = W::kSumInSmem ? reinterpret_cast<float*>(sm + W::kOffSum)
+                                            : p.sums + static_cast<size_t>(blockIdx.x) * D * W::kUnitRows;
+                return *reinterpret_cast<float4*>(sums + c * W::kUnitRows + 4 * row);
             };
             float sum_m = -INFINITY;
             bool has_sums = false;
@@ -515,22 +511,13 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                         __syncwarp();
                         tmem_read16(o_at + c, w);
                         if (row < rows) {
-                            alignas(16) float y[16];
-                            if (has_sums) {
-                                get_sums(c, y);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) y[i] = fmaf(y[i], f, __uint_as_float(w[i]));
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(w[i]);
-                            }
-                            if constexpr (W::kSumInSmem) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) sums[(c + i) * kRows] = y[i];
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 16; i += 4)
-                                    *reinterpret_cast<float4*>(sums + c + i) = *reinterpret_cast<const float4*>(y + i);
+                            for (int i = 0; i < 16; i += 4) {
+                                const float4 y = has_sums ? four_sums(c + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                four_sums(c + i) = make_float4(fmaf(y.x, f, __uint_as_float(w[i])),
+                                                               fmaf(y.y, f, __uint_as_float(w[i + 1])),
+                                                               fmaf(y.z, f, __uint_as_float(w[i + 2])),
+                                                               fmaf(y.w, f, __uint_as_float(w[i + 3])));
                             }
                         }
                     }
@@ -633,10 +620,14 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(w[i]);
                     if (has_sums && row < rows) {
-                        alignas(16) float y[16];
-                        get_sums(c, y);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = fmaf(y[i], f, o[i]);
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 y = four_sums(c + i);
+                            o[i] = fmaf(y.x, f, o[i]);
+                            o[i + 1] = fmaf(y.y, f, o[i + 1]);
+                            o[i + 2] = fmaf(y.z, f, o[i + 2]);
+                            o[i + 3] = fmaf(y.w, f, o[i + 3]);
+                        }
                     }
                     if (row < rows && done) {
                         store_out16(p, out + c, o, inv);
@@ -1002,8 +993,7 @@ template <int D>
 cudaError_t launch_dim(const AttnParams& p, cudaStream_t stream) {
     const bool split = p.dtype == DType::kF32;
     if constexpr (D <= 128) {
-        if (static_cast<long long>(p.c.T) * p.group > kRows)
-            return split ? launch_one<D, true, 2>(p, stream) : launch_one<D, false, 2>(p, stream);
+        if (!split && static_cast<long long>(p.c.T) * p.group > kRows) return launch_one<D, false, 2>(p, stream);
     }
     return split ? launch_one<D, true, 1>(p, stream) : launch_one<D, false, 1>(p, stream);
 }
@@ -1011,11 +1001,12 @@ cudaError_t launch_dim(const AttnParams& p, cudaStream_t stream) {
 }  // namespace
 
 size_t kv4_window_workspace_bytes(int head_dim) {
-    return static_cast<size_t>(2 * kMaxSms) * (2 * kRows * (head_dim + 2) * sizeof(float) + sizeof(JoinRecord));
+    return static_cast<size_t>(2 * kMaxSms) * ((2 * kRows * (head_dim + 2) + kRows * head_dim) * sizeof(float) + sizeof(JoinRecord));
 }
 
 cudaError_t launch_kv4_window(AttnParams p, cudaStream_t stream) {
-    p.records = p.part + static_cast<size_t>(2 * kMaxSms) * 2 * kRows * (p.c.head_dim + 2);
+    p.sums = p.part + static_cast<size_t>(2 * kMaxSms) * 2 * kRows * (p.c.head_dim + 2);
+    p.records = p.sums + static_cast<size_t>(2 * kMaxSms) * kRows * p.c.head_dim;
     switch (p.c.head_dim) {
         case 64: return launch_dim<64>(p, stream);
         case 128: return launch_dim<128>(p, stream);
