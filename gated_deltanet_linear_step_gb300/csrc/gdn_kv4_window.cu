@@ -486,7 +486,6 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             const int lim = row < rows ? min(x.start + (x.col0 + row) / p.group, x.end - 1) : -1;
             const int seen_by_all = min(x.start + x.col0 / p.group + 1, x.end);
             float m = -INFINITY, shift = kNone, l = 0.0f;
-            float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kUnitRows * (D + 2));
             // sums of earlier tiles, relative to sum_m
             auto four_sums = [&](int c) -> float4& {  // of dims c .. c + 3
                 float* sums = W::kSumInSmem ? reinterpret_cast<float*>(sm + W::kOffSum)
@@ -494,17 +493,91 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                 return *reinterpret_cast<float4*>(sums + c * W::kUnitRows + 4 * row);
             };
             float sum_m = -INFINITY;
-            bool has_sums = false;
-            // the factor of those sums now
-            auto sums_factor = [&]() -> float { return sum_m == -INFINITY ? 0.0f : exp2_approx(sum_m - m); };
-            for (int r = r0; r < r1; ++r, ++n) {
-                if (!failed && !warp_wait(s_done + 16 * block + 8 * (n & 1), tile_parity(n))) failed = true;
-                tc_fence_after();
-                const bool fresh = (r - r0) % W::kFreshTiles == 0;  // the sums in tensor memory start with this tile
-                if (some && fresh && r > r0) {
-                    if (!failed && !warp_wait(o_done + 16 * block + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
+            for (int r = r0; r < r1;) {
+                const int first = r, last = min(first + W::kFreshTiles, r1);
+                for (; r < last; ++r, ++n) {
+                    if (!failed && !warp_wait(s_done + 16 * block + 8 * (n & 1), tile_parity(n))) failed = true;
                     tc_fence_after();
-                    const float f = sums_factor();
+                    if (some) {
+                        constexpr int kHalf = kTok / 2, kChunks = kHalf / 32;
+                        // the half's scores, then, per 32 of them, 16 columns of probabilities and 16 of their rests
+                        const uint32_t s_at = lanes + 128 * block + kTok * (n % kBuffers) + kHalf * half;
+                        const int p0 = r * kTok + kHalf * half;  // its first position
+                        const uint32_t bad = (bad_s[n & 3] >> (kHalf / 16 * half)) & ((1u << (kHalf / 16)) - 1u);
+                        const bool part = p0 + kHalf > seen_by_all || bad != 0;
+                        float s[32];
+                        auto scores = [&](int c) {
+                            tmem_read32(s_at + 32 * c, s);
+                            if (part) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (p0 + 32 * c + i > lim || ((bad >> (2 * c + (i >> 4))) & 1u)) s[i] = -INFINITY;
+                            }
+                        };
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c) {
+                            scores(c);
+                            float t0 = max3(s[0], s[1], s[2]), t1 = max3(s[3], s[4], s[5]);
+#pragma unroll
+                            for (int i = 6; i < 30; i += 4) {
+                                t0 = max3(t0, s[i], s[i + 1]);
+                                t1 = max3(t1, s[i + 2], s[i + 3]);
+                            }
+                            top = max3(top, max3(t0, s[30], s[31]), t1);
+                        }
+                        top = fmaxf(top, exchange(top));
+                        if (__any_sync(~0u, fmaf(top, mul, shift) > kPShift + kSlack)) {
+                            const float v = fmaxf(m, top * mul);
+                            const float al = v == m ? 1.0f : exp2_approx(m - v);
+                            m = v;
+                            shift = v == -INFINITY ? kNone : kPShift - v;
+                            l *= al;
+                            if (r > first) {  // this half of the sums so far: after the product that is adding to them
+                                if (!failed && !warp_wait(o_done + 16 * block + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                                    uint32_t w[16];
+                                    tmem_read16(o_at + c, w);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * al);
+                                    tmem_st16(o_at + c, w);
+                                }
+                            }
+                        }
+                        float2 sum = make_float2(0.0f, 0.0f);
+                        const float2 mul2 = make_float2(mul, mul), shift2 = make_float2(shift, shift);
+#pragma unroll
+                        for (int c = kChunks - 1; c >= 0; --c) {  // the last chunk is still in registers
+                            if (c < kChunks - 1) scores(c);
+                            uint32_t hi[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), mul2, shift2);
+                                s[2 * i] = exp2_approx(e.x);
+                                s[2 * i + 1] = exp2_approx(e.y);
+                                sum = __fadd2_rn(sum, make_float2(s[2 * i], s[2 * i + 1]));
+                                hi[i] = pack_half2(s[2 * i], s[2 * i + 1]);
+                            }
+                            tmem_st16(s_at + 32 * c, hi);
+                            if constexpr (SPLIT) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) hi[i] = pack_rest(s[2 * i], s[2 * i + 1], hi[i]);
+                                tmem_st16(s_at + 32 * c + 16, hi);
+                            }
+                        }
+                        l += sum.x + sum.y;
+                        tmem_st_wait();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_local(p_ready + 16 * block + 8 * (n & 1));
+                }
+                if (!failed && !warp_wait(o_done + 16 * block + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
+                tc_fence_after();
+                if (some && r1 - r0 > W::kFreshTiles) {  // these sums and the earlier ones; the last time in tensor memory
+                    const float f = sum_m == -INFINITY ? 0.0f : exp2_approx(sum_m - m);
 #pragma unroll 1
                     for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
                         uint32_t w[16];
@@ -513,102 +586,27 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                         if (row < rows) {
 #pragma unroll
                             for (int i = 0; i < 16; i += 4) {
-                                const float4 y = has_sums ? four_sums(c + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                                four_sums(c + i) = make_float4(fmaf(y.x, f, __uint_as_float(w[i])),
-                                                               fmaf(y.y, f, __uint_as_float(w[i + 1])),
-                                                               fmaf(y.z, f, __uint_as_float(w[i + 2])),
-                                                               fmaf(y.w, f, __uint_as_float(w[i + 3])));
+                                const float4 y = first > r0 ? four_sums(c + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                const float4 v = make_float4(fmaf(y.x, f, __uint_as_float(w[i])), fmaf(y.y, f, __uint_as_float(w[i + 1])),
+                                                             fmaf(y.z, f, __uint_as_float(w[i + 2])), fmaf(y.w, f, __uint_as_float(w[i + 3])));
+                                w[i] = __float_as_uint(v.x), w[i + 1] = __float_as_uint(v.y);
+                                w[i + 2] = __float_as_uint(v.z), w[i + 3] = __float_as_uint(v.w);
+                                if (last < r1) four_sums(c + i) = v;
                             }
                         }
+                        __syncwarp();
+                        if (last == r1) tmem_st16(o_at + c, w);
                     }
-                    __syncwarp();
-                    sum_m = m;
-                    has_sums = true;
-                }
-                if (some) {
-                    constexpr int kHalf = kTok / 2, kChunks = kHalf / 32;
-                    // the half's scores, then, per 32 of them, 16 columns of probabilities and 16 of their rests
-                    const uint32_t s_at = lanes + 128 * block + kTok * (n % kBuffers) + kHalf * half;
-                    const int p0 = r * kTok + kHalf * half;  // its first position
-                    const uint32_t bad = (bad_s[n & 3] >> (kHalf / 16 * half)) & ((1u << (kHalf / 16)) - 1u);
-                    const bool part = p0 + kHalf > seen_by_all || bad != 0;
-                    float s[32];
-                    auto scores = [&](int c) {
-                        tmem_read32(s_at + 32 * c, s);
-                        if (part) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (p0 + 32 * c + i > lim || ((bad >> (2 * c + (i >> 4))) & 1u)) s[i] = -INFINITY;
-                        }
-                    };
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        scores(c);
-                        float t0 = max3(s[0], s[1], s[2]), t1 = max3(s[3], s[4], s[5]);
-#pragma unroll
-                        for (int i = 6; i < 30; i += 4) {
-                            t0 = max3(t0, s[i], s[i + 1]);
-                            t1 = max3(t1, s[i + 2], s[i + 3]);
-                        }
-                        top = max3(top, max3(t0, s[30], s[31]), t1);
-                    }
-                    top = fmaxf(top, exchange(top));
-                    if (__any_sync(~0u, fmaf(top, mul, shift) > kPShift + kSlack)) {
-                        const float v = fmaxf(m, top * mul);
-                        const float al = v == m ? 1.0f : exp2_approx(m - v);
-                        m = v;
-                        shift = v == -INFINITY ? kNone : kPShift - v;
-                        l *= al;
-                        if (!fresh) {  // this half of the sums so far: after the product that is adding to them
-                            if (!failed && !warp_wait(o_done + 16 * block + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
-                                uint32_t w[16];
-                                tmem_read16(o_at + c, w);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * al);
-                                tmem_st16(o_at + c, w);
-                            }
-                        }
-                    }
-                    float2 sum = make_float2(0.0f, 0.0f);
-                    const float2 mul2 = make_float2(mul, mul), shift2 = make_float2(shift, shift);
-#pragma unroll
-                    for (int c = kChunks - 1; c >= 0; --c) {  // the last chunk is still in registers
-                        if (c < kChunks - 1) scores(c);
-                        uint32_t hi[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), mul2, shift2);
-                            s[2 * i] = exp2_approx(e.x);
-                            s[2 * i + 1] = exp2_approx(e.y);
-                            sum = __fadd2_rn(sum, make_float2(s[2 * i], s[2 * i + 1]));
-                            hi[i] = pack_half2(s[2 * i], s[2 * i + 1]);
-                        }
-                        tmem_st16(s_at + 32 * c, hi);
-                        if constexpr (SPLIT) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) hi[i] = pack_rest(s[2 * i], s[2 * i + 1], hi[i]);
-                            tmem_st16(s_at + 32 * c + 16, hi);
-                        }
-                    }
-                    l += sum.x + sum.y;
                     tmem_st_wait();
+                    sum_m = m;
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_local(p_ready + 16 * block + 8 * (n & 1));
             }
             // outputs: each half its dims
             const float other = exchange(l);
             l = half == 0 ? l + other : other + l;
-            if (!failed && !warp_wait(o_done + 16 * block + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;
-            tc_fence_after();
             const bool done = r0 == 0 && r1 == cur.cost - (kStartTokens >> p.tile_shift);
             if (some) {
-                const float f = sums_factor();
+                float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kUnitRows * (D + 2));
                 const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // no key at all: zeros
                 const size_t out = row < rows ? q_row(p, b, x, x.col0 + row) : 0;
 #pragma unroll 1
@@ -619,16 +617,6 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                     float o[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(w[i]);
-                    if (has_sums && row < rows) {
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 y = four_sums(c + i);
-                            o[i] = fmaf(y.x, f, o[i]);
-                            o[i + 1] = fmaf(y.y, f, o[i + 1]);
-                            o[i + 2] = fmaf(y.z, f, o[i + 2]);
-                            o[i + 3] = fmaf(y.w, f, o[i + 3]);
-                        }
-                    }
                     if (row < rows && done) {
                         store_out16(p, out + c, o, inv);
                     } else if (row < rows) {
