@@ -8,8 +8,8 @@
 // keys and values serves the whole group of a block of tokens, and two blocks of 128 rows
 // (256 rows per CTA) where a window has them.
 //
-// What bounds it. 2 x 1024 tokens behind 8000, 32 query heads of 128, bf16: 330 us, 0.87 PFLOP/s, 0.44 of the
-// measured bf16 rate. For a 64-token tile of both blocks (2900 clocks of an SM) the tensor pipe works 1500 clocks (a product
+// What bounds it. 2 x 1024 tokens behind 8000, 32 query heads of 128, bf16: 310 us, 0.92 PFLOP/s, 0.46 of the
+// measured bf16 rate (four sequences 605 us, 0.94 PFLOP/s). For a 64-token tile of both blocks (2900 clocks of an SM) the tensor pipe works 1500 clocks (a product
 // of 64 columns takes as long as one of 128), the special-function unit 1024 (16384 exponentials), and the schedulers issue
 // 0.55 of the time; the longest chain is a softmax warp's own: scores from tensor memory, maximum, exchange,
 // exponentials, probabilities back, about 2200 clocks. Windows of few rows (a verify window, 17 query heads)
@@ -622,7 +622,8 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                     } else if (row < rows) {
 #pragma unroll
                         for (int i = 0; i < 16; i += 4)
-                            *reinterpret_cast<float4*>(slot + row * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            *reinterpret_cast<float4*>(slot + (NB == 2 ? (c + i) * kUnitRows + 4 * row : row * D + c + i)) =
+                                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     }
                 }
                 if (!done && half == 0 && row < rows) {
@@ -881,15 +882,16 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
     }
 }
 
-// CTAs that join a unit. A window of 32 tokens after 30000 (19 parts a unit) takes 137 / 95 / 74 us with 4 / 8 / 16, and
-// 61 us with a part's factor computed once, by one lane; 2 x 1024 tokens from position 0: 88 / 83 / 83, 82 us.
-constexpr int kJoinCtas = 16;
-
 // Joins the partial results of the units that several CTAs shared: a column of blocks for each CTA that such a unit
-// starts in, a warp for each row.
-template <int D>
+// starts in. Two blocks of rows: a warp for 32 rows and 16 dims, the sums lying as [dim / 4][row][4], so that a warp here
+// reads, and the softmax warps wrote, whole lines. One block: a warp for each row, the sums lying as [row][dim]; units of
+// few rows have more parts. 2 x 1024 tokens after 8000, 32 heads of 128: 310 us by the first way, 321 us by the second
+// (of 64: 234 and 241, from position 0: 76 and 82); 16 ragged windows of 8 tokens with 5 heads: 51 and 49 us, 32 tokens
+// after 30000: 64 and 60 us. By rows, CTAs per unit: the last case takes 137 / 95 / 74 us with 4 / 8 / 16, and 61 us with
+// a part's factor computed once, by one lane.
+template <int D, int NB>
 __global__ void __launch_bounds__(256) kv4_window_join_kernel(const __grid_constant__ AttnParams p) {
-    const size_t unit = p.unit_rows, slot_floats = unit * (D + 2);
+    constexpr size_t unit = NB * kRows, slot_floats = unit * (D + 2);
     const int lane = threadIdx.x & 31;
     griddep_wait();
     const JoinRecord rec = reinterpret_cast<const JoinRecord*>(p.records)[blockIdx.x];
@@ -901,6 +903,34 @@ __global__ void __launch_bounds__(256) kv4_window_join_kernel(const __grid_const
     auto slot = [&](int i) -> const float* {
         return base + (i == 0 ? 1 : 2 * static_cast<size_t>(i)) * slot_floats;
     };
+    if constexpr (NB == 2) {
+        const int items = (rows + 31) / 32 * (D / 16);
+        for (int item = blockIdx.y * 8 + (threadIdx.x >> 5); item < items; item += gridDim.y * 8) {
+            const int row = item / (D / 16) * 32 + lane, c = item % (D / 16) * 16;
+            if (row >= rows) continue;
+            float mm = -INFINITY;
+#pragma unroll 8
+            for (int i = 0; i < rec.parts; ++i) mm = fmaxf(mm, slot(i)[unit * D + row]);
+            float o[16] = {}, l = 0.0f;
+#pragma unroll 4
+            for (int i = 0; i < rec.parts; ++i) {
+                const float* s = slot(i);
+                const float ms = s[unit * D + row];
+                const float f = ms == -INFINITY ? 0.0f : exp2_approx(ms - mm);
+                l += s[unit * D + unit + row] * f;
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(s + (c + j) * unit + 4 * row);
+                    o[j] += y.x * f;
+                    o[j + 1] += y.y * f;
+                    o[j + 2] += y.z * f;
+                    o[j + 3] += y.w * f;
+                }
+            }
+            store_out16(p, q_row(p, k.b, x, x.col0 + row) + c, o, l > 0.0f || l != l ? 1.0f / l : 0.0f);
+        }
+        return;
+    }
     for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < rows; row += gridDim.y * 8) {
         // a lane has the maximum and sum of every 32nd part; a part's factor is asked of its lane
         float ms = lane < rec.parts ? slot(lane)[unit * D + row] : -INFINITY;
@@ -966,7 +996,9 @@ cudaError_t launch_one(AttnParams p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const long long rows = std::min<long long>(static_cast<long long>(p.c.T) * p.group, W::kUnitRows);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, static_cast<unsigned>(std::min<long long>((rows + 7) / 8, kJoinCtas)));
+    cfg.gridDim = dim3(ctas, static_cast<unsigned>(NB == 2
+                                                       ? ((rows + 31) / 32 * (D / 16) + 7) / 8
+                                                       : std::min<long long>((rows + 7) / 8, 16)));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -974,7 +1006,7 @@ cudaError_t launch_one(AttnParams p, cudaStream_t stream) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_window_join_kernel<D>, p);
+    return cudaLaunchKernelEx(&cfg, kv4_window_join_kernel<D, NB>, p);
 }
 
 template <int D>
