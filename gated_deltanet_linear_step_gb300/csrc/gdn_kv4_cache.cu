@@ -8,8 +8,8 @@
 // land in contiguous 256- and 32-byte pieces. Reading: 16 bytes of output
 // per place, so every store of a warp is one contiguous 512-byte piece.
 //
-// Measured: 16 x 1024 ragged tokens of 4 layers, 8 heads of 128, bf16 (127 MB in, 36 MB of cache written): 39 us, 0.62 of
-// the measured HBM rate; with correctly rounded quotients, as fp32 values still take, 52 us. One token of 64
+// Measured: 16 x 1024 ragged tokens of 4 layers, 8 heads of 128, bf16 (127 MB in, 36 MB of cache written): 35 us, 0.69 of
+// the measured HBM rate; with correctly rounded quotients, as fp32 values still take, 13 us more. One token of 64
 // sequences, written and read back: 5 us, two launches and the latency of three dependent reads each.
 
 #include "gdn_kv4.cuh"
@@ -43,15 +43,6 @@ struct CacheParams {
     uint32_t rows;  // B L kv_heads T
 };
 
-// 16 consecutive values as floats.
-__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(p) + i);
-        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-    }
-}
-
 template <typename T>
 __device__ __forceinline__ float2 pair_of(uint32_t w);
 template <>
@@ -63,20 +54,31 @@ __device__ __forceinline__ float2 pair_of<__nv_bfloat16>(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// 16 consecutive values, as they are and as floats.
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
+struct Raw16 {
+    uint4 v[sizeof(T)];
+    __device__ __forceinline__ explicit Raw16(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) v[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    }
+    __device__ __forceinline__ void floats(float (&x)[16]) const {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = pair_of<T>(w[j]);
-            x[8 * i + 2 * j] = f.x;
-            x[8 * i + 2 * j + 1] = f.y;
+        for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(T) == 4) {
+                    x[4 * i + j] = __uint_as_float(w[j]);
+                } else {
+                    const float2 f = pair_of<T>(w[j]);
+                    x[8 * i + 2 * j] = f.x;
+                    x[8 * i + 2 * j + 1] = f.y;
+                }
+            }
         }
     }
-}
+};
 
 // max of two magnitudes; NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -147,8 +149,10 @@ __device__ __forceinline__ uint32_t quantise16(float (&x)[16], uint2& codes) {
     return byte;
 }
 
+// Six CTAs per SM for 16-bit values, 40 registers (fp32 ones, which wait for their correctly rounded quotients, are
+// slower so: 128 against 117 us): 16 x 1024 ragged tokens of 4 layers, 8 heads of 128, written and read back, 74.2 -> 69.9 us.
 template <typename T, int D>
-__global__ void __launch_bounds__(kCacheThreads) kv4_append_kernel(const __grid_constant__ CacheParams p) {
+__global__ void __launch_bounds__(kCacheThreads, sizeof(T) == 4 ? 1 : 6) kv4_append_kernel(const __grid_constant__ CacheParams p) {
     constexpr int kBlocks = D / 16;
     const unsigned long long item = static_cast<unsigned long long>(blockIdx.x) * kCacheThreads + threadIdx.x;
     const int blk = static_cast<int>(item) & (kBlocks - 1);
@@ -163,9 +167,7 @@ __global__ void __launch_bounds__(kCacheThreads) kv4_append_kernel(const __grid_
     const Kv4Window w = kv4_window(p.c, b);
     if (t >= w.n) return;
     const size_t src = ((static_cast<size_t>(bl) * p.c.T + t) * p.c.kv_heads + h) * D + blk * 16;
-    float k[16], v[16];
-    load16(static_cast<const T*>(p.in_k) + src, k);
-    load16(static_cast<const T*>(p.in_v) + src, v);
+    const Raw16<T> k(static_cast<const T*>(p.in_k) + src), v(static_cast<const T*>(p.in_v) + src);
     const int page = t < w.cap - w.start ? kv4_page(p.c, b, w.start + t) : -1;
     if (page < 0) {
         if (blk == 0) atomicOr(&g_kv4_cache_error, kErrBadPage);
@@ -178,10 +180,13 @@ __global__ void __launch_bounds__(kCacheThreads) kv4_append_kernel(const __grid_
     const int code_at = r * (D / 2) + (blk ^ kv4_swizzle(r, kBlocks)) * 8;
     const int scale_at = psize * (D / 2) + r * kBlocks + blk;
     uint2 codes;
-    uint32_t s = quantise16<T>(k, codes);
+    float x[16];
+    k.floats(x);
+    uint32_t s = quantise16<T>(x, codes);
     *reinterpret_cast<uint2*>(kc + code_at) = codes;
     kc[scale_at] = static_cast<uint8_t>(s);
-    s = quantise16<T>(v, codes);
+    v.floats(x);
+    s = quantise16<T>(x, codes);
     *reinterpret_cast<uint2*>(vc + code_at) = codes;
     vc[scale_at] = static_cast<uint8_t>(s);
 }
