@@ -172,3 +172,36 @@ def test_long_16_bit_sums(cuda_device, dtype, T, D):
     error = (out - want).abs()
     print("largest error %.2e" % (error / want.abs()).nan_to_num().max().item())
     assert (error <= tolerance * want.abs() + info.smallest_normal * info.eps / 2).all()
+
+
+@pytest.mark.parametrize("dtype,T,D", [("fp32", 20, 64), ("fp32", 33, 128), ("fp32", 17, 256), ("bf16", 150, 64)])
+def test_maxima_that_rise_over_long_rows(cuda_device, dtype, T, D):
+    """Keys that grow with their position, so that the maximum rises after the sums were started afresh, and enough
+    heads that a sequence is not split; against fp64 over the values that the cache gives back. Tolerances as in
+    test_gpu_kv4.py, from each row's own largest score and sum |q k|; and, as these rows are nearly all one key's, half
+    of fp16's smallest step for each probability relative to 2^-8 of the largest: 2^-33."""
+    heads, keys = 310, 1700
+    c = Cache(cuda_device, 1, 1, heads, D, 32, keys)
+    ramp = (0.1 + torch.arange(keys, device=cuda_device) / 800).view(1, 1, keys, 1, 1)
+    k = (values((1, 1, keys, heads, D), "fp32", cuda_device, 31) * ramp).to(TYPES[dtype])
+    v = values((1, 1, keys, heads, D), dtype, cuda_device, 32)
+    c.append(k, v, [0])
+    q = values((1, 1, T, heads, D), dtype, cuda_device, 33)
+    out = c.attend(q, [keys - T])
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    c.g.gdn_kv4_read(c.t_cache, c.t_table, c.i32([0]), ko, vo, c.page)
+    q, k, v, out = (x[0, 0].transpose(0, 1).double() for x in (q, ko, vo, out))  # [head][token][dim]
+    scale = D ** -0.5
+    seen = torch.arange(keys, device=cuda_device) <= keys - T + torch.arange(T, device=cuda_device).view(T, 1)
+    s = (scale * q @ k.transpose(1, 2)).masked_fill(~seen, -float("inf"))
+    p = s.softmax(-1)
+    want, amount = p @ v, p @ v.abs()
+    products = (scale * q.abs() @ k.abs().transpose(1, 2)).masked_fill(~seen, 0).amax(-1, keepdim=True)
+    largest = s.masked_fill(~seen, 0).abs().amax(-1, keepdim=True)
+    rounding = 2**-22 if dtype == "fp32" else 2**-12
+    score = (D + 8) * 2**-24 * products + 2**-22 * (2 + largest)
+    tolerance = torch.finfo(TYPES[dtype]).eps / 2 * want.abs() + amount * (rounding + 2 * score + 2 * keys * 2**-24)
+    tolerance = tolerance + 2**-33 * (seen.double() @ v.abs())
+    ratio = ((out - want).abs() / tolerance).max().item()
+    print("largest error %.3f of the tolerance" % ratio)
+    assert ratio <= 1
