@@ -9,12 +9,12 @@
 // (256 rows per CTA) where a window has them.
 //
 // What bounds it. 2 x 1024 tokens behind 8000, 32 query heads of 128, bf16: 310 us, 0.92 PFLOP/s, 0.46 of the
-// measured bf16 rate (four sequences 605 us, 0.94 PFLOP/s). For a 64-token tile of both blocks (2900 clocks of an SM) the tensor pipe works 1500 clocks (a product
-// of 64 columns takes as long as one of 128), the special-function unit 1024 (16384 exponentials), and the schedulers issue
-// 0.55 of the time; the longest chain is a softmax warp's own: scores from tensor memory, maximum, exchange,
-// exponentials, probabilities back, about 2200 clocks. Windows of few rows (a verify window, 17 query heads)
-// are bound by the latency of one tile's steps, about 2600 clocks, which is why up to 16 rows go to
-// gdn_kv4_attention.cu (64 sequences of 4096, 16 rows: 62 us there, 104 us here).
+// measured bf16 rate (four sequences 605 us, 0.94 PFLOP/s). For a 64-token tile of both blocks (2750 clocks of an SM) the
+// tensor pipe works 1500 clocks (a product of 64 columns takes as long as one of 128), the special-function unit 1024
+// (16384 exponentials), and the schedulers issue 0.57 of the time; the longest chain is a softmax warp's own: scores
+// from tensor memory, maximum, exchange, exponentials, probabilities back, about 2200 clocks. Windows of few rows (a
+// verify window, 17 query heads) are bound by the latency of one tile's steps, about 2600 clocks, which is why up to 16
+// rows go to gdn_kv4_attention.cu (64 sequences of 4096, 16 rows: 62 us there, 104 us here).
 //
 //   warp 0     issues the products, by an elected lane (a lane chosen by its number had each product's operands moved to
 //              uniform registers by a loop over the lanes, and issuing took longer than everything else: 411 us)
