@@ -327,9 +327,9 @@ __global__ void __launch_bounds__(kLpThreads, 8) logprobs_kernel(const LogprobAr
         if (tid < kMaxK) best[tid] = 0;
         __syncthreads();
         const int n = count;
-        if (n <= kList) {
-            if (tid < n) {
-                const unsigned long long me = list[tid];
+        if (n <= kList) {  // (the list is longer than the CTA has threads)
+            for (int j = tid; j < n; j += kLpThreads) {
+                const unsigned long long me = list[j];
                 int place = 0;
                 for (int i = 0; i < n; ++i) place += list[i] > me;
                 if (place < k) best[place] = me;
