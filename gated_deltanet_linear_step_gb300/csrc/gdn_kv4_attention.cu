@@ -28,9 +28,9 @@
 // Numerics. Queries are scaled by a power of two per row to fill fp16's range
 // (16-bit inputs stay exact; fp32 ones are split into fp16 hi + lo, 22 bits);
 // scores, maxima, sums and outputs are fp32. Probabilities are rounded to fp16
-// (half a step is 2^-12 of the value, below the 2^-9 of a bf16 output; the reference maximum stands for 2^8, so that small ones
-// keep their bits) or, for fp32, split into hi + lo. Below 2^-22 (hi + lo: 2^-11) of the row's largest they lose bits to fp16's
-// smallest step, 2^-33 of the largest at most. Masked keys take no part: their
+// (half a step is 2^-12 of the value, below the 2^-9 of a bf16 output; the reference maximum stands for 2^9, so that small ones
+// keep their bits) or, for fp32, split into hi + lo. Below 2^-23 (hi + lo: 2^-12) of the row's largest they lose bits to fp16's
+// smallest step, 2^-34 of the largest at most. Masked keys take no part: their
 // scores are set to -inf by a select, and the scales of tokens past the end
 // are set to zero, so whatever such bytes hold (infinities, NaN) does not matter.
 //

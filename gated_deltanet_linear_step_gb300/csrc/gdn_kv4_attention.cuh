@@ -7,8 +7,8 @@
 
 namespace gdn {
 
-constexpr float kPShift = 8.0f;  // probabilities are kept relative to 2^-8 of the reference maximum ...
-constexpr float kSlack = 6.0f;   // ... which is raised when a score exceeds it by 6: none is above 2^14
+constexpr float kPShift = 9.0f;  // probabilities are kept relative to 2^-9 of the reference maximum's ...
+constexpr float kSlack = 6.0f;   // ... which is raised when a score exceeds it by 6: none is above 2^15
 constexpr float kNone = 1e30f;   // the shift of a column that has seen no key
 
 // The unit, if there is one, whose first rounds a CTA did and whose last ones other CTAs did: what the joining kernel
