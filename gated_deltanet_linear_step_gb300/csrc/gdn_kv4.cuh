@@ -41,8 +41,11 @@ __host__ __device__ constexpr size_t kv4_head_bytes(int page, int head_dim) {
     return static_cast<size_t>(2) * page * (head_dim / 2 + head_dim / 16);
 }
 
+constexpr int kKv4MaxTokens = 1 << 20;  // of a window
+
 // Where sequence b's window lies: its first position, its valid tokens, and the end of
-// the positions that the block table can hold.
+// the positions that the block table can hold. A first position below 0 stays so (no lower than
+// -kKv4MaxTokens, where no token reaches position 0): its tokens before position 0 are missing.
 struct Kv4Window {
     int start, n, cap;
 };
@@ -60,7 +63,7 @@ struct Kv4Cache {
 __device__ __forceinline__ Kv4Window kv4_window(const Kv4Cache& c, int b) {
     Kv4Window w;
     w.cap = c.max_pages << c.page_shift;
-    w.start = min(max(__ldg(c.kv_start + b), 0), w.cap);
+    w.start = min(max(__ldg(c.kv_start + b), -kKv4MaxTokens), w.cap);
     w.n = c.seq_len != nullptr ? min(max(__ldg(c.seq_len + b), 0), c.T) : c.T;
     return w;
 }
@@ -68,7 +71,7 @@ __device__ __forceinline__ Kv4Window kv4_window(const Kv4Cache& c, int b) {
 // The page that holds position pos of sequence b, or -1.
 __device__ __forceinline__ int kv4_page(const Kv4Cache& c, int b, int pos) {
     const int slot = pos >> c.page_shift;
-    if (slot >= c.max_pages) return -1;
+    if (static_cast<uint32_t>(slot) >= static_cast<uint32_t>(c.max_pages)) return -1;
     const int page = __ldg(c.block_table + static_cast<size_t>(b) * c.max_pages + slot);
     return page >= 0 && page < c.n_pages ? page : -1;
 }
@@ -78,6 +81,9 @@ __device__ __forceinline__ size_t kv4_head_offset(const Kv4Cache& c, int l, int 
     return ((static_cast<size_t>(l) * c.n_pages + page) * c.kv_heads + h) *
            kv4_head_bytes(1 << c.page_shift, c.head_dim);
 }
+
+// Whether tokens of the window lie outside the positions that the block table can hold.
+__device__ __forceinline__ bool kv4_runs_out(const Kv4Window& w) { return w.n > 0 && (w.start < 0 || w.n > w.cap - w.start); }
 
 #endif  // __CUDACC__
 

@@ -90,7 +90,7 @@ template <int D>
 __device__ __forceinline__ int seq_cost(const Kv4Cache& c, int b) {
     const Kv4Window w = kv4_window(c, b);
     if (w.n == 0) return 0;
-    const int end = w.start + min(w.n, w.cap - w.start);
+    const int end = max(w.start + min(w.n, w.cap - w.start), 1);  // one round at least: its rows get their zeros
     constexpr int kRound = Tile<D>::kTokens * kWarps;
     return kUnitCost + (end + kRound - 1) / kRound;
 }
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
 
         // --- queries of the unit: B fragments in shared memory, or straight in registers
         const int all_cols = min(x.n * p.group - x.col0, kCols);  // columns that exist (<= 0: none)
-        if (tid == 0 && x.n > kv4_window(p.c, b).cap - x.start) atomicOr(&g_kv4_attn_error, kErrBadPage);
+        if (tid == 0 && kv4_runs_out(kv4_window(p.c, b))) atomicOr(&g_kv4_attn_error, kErrBadPage);
         uint2 qr[kQRegs ? D / 16 : 1];
         float col_mul = 0.0f;  // of column g
         if constexpr (kQRegs) {

@@ -32,7 +32,7 @@ struct AttnParams {
 
 // A unit: its layer, kv head, first column, and the positions its columns see.
 struct Unit {
-    int l, h, col0, start, n, end;  // end: first position that no column sees
+    int l, h, col0, start, n, end;  // end: first position that no column sees (not above 0: there is none that one sees)
 };
 
 // ------------------------------------------------------------ work split --

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kCacheThreads) kv4_read_kernel(const __grid_co
     for (int i = 0; i < kReadItems; ++i) {
         const Kv4Window w = kv4_window(p.c, b[i]);
         on[i] = on[i] && t[i] < w.n;
-        pos[i] = t[i] < w.cap - w.start ? w.start + t[i] : -1;
+        pos[i] = t[i] < w.cap - w.start ? w.start + t[i] : -1;  // below 0: not in the table
     }
 #pragma unroll
     for (int i = 0; i < kReadItems; ++i) page[i] = on[i] && pos[i] >= 0 ? kv4_page(p.c, b[i], pos[i]) : -1;

@@ -114,17 +114,20 @@ struct WinCursor {
     int left;
 };
 
-// First position that no row of block blk sees (0: no row).
+constexpr int kNoRow = -2147483647 - 1;
+
+// First position that no row of block blk sees, or kNoRow.
 __device__ __forceinline__ int block_end(const AttnParams& p, const Kv4Window& w, int blk) {
     const int row = blk * p.unit_rows;  // T group < 2^31
-    if (row >= w.n * p.group) return 0;
+    if (row >= w.n * p.group) return kNoRow;
     const int t_hi = min(static_cast<int>((static_cast<uint32_t>(row) + p.unit_rows - 1) / p.group), w.n - 1);
     return w.start + min(t_hi + 1, w.cap - w.start);
 }
 
 __device__ __forceinline__ int block_cost(const AttnParams& p, const Kv4Window& w, int blk) {
     const int end = block_end(p, w, blk);
-    return end == 0 ? 0 : (kStartTokens + end + (1 << p.tile_shift) - 1) >> p.tile_shift;
+    // one tile at least: rows that see no position get their zeros
+    return end == kNoRow ? 0 : (kStartTokens + max(end, 1) + (1 << p.tile_shift) - 1) >> p.tile_shift;
 }
 
 // Cost of block i % col_blocks of sequence i / col_blocks.
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             const Unit x = win_unit(p, cur);
             const int b = cur.b;
             const int rows = min(x.n * p.group - x.col0, kUnitRows);
-            if (tid == 32 && x.n > kv4_window(p.c, b).cap - x.start) atomicOr(&g_kv4_window_error, kErrBadPage);
+            if (tid == 32 && kv4_runs_out(kv4_window(p.c, b))) atomicOr(&g_kv4_window_error, kErrBadPage);
             // queries, scaled to fill fp16's range: row 8 i + this warp of the block's eight, kAtOnce rows in flight
             constexpr int kAtOnce = D > 128 ? 2 : 4;
             const int mine = 128 * block + ((warp - 1) & 7);

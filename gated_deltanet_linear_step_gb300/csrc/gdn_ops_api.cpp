@@ -12,6 +12,7 @@
 static_assert(GDN_DTYPE_F32 == static_cast<int>(gdn::DType::kF32) && GDN_DTYPE_F16 == static_cast<int>(gdn::DType::kF16) &&
                   GDN_DTYPE_BF16 == static_cast<int>(gdn::DType::kBF16),
               "data type mismatch");
+static_assert(GDN_KV4_MAX_T == gdn::kKv4MaxTokens, "window size mismatch");
 
 namespace gdn {
 gdn_status report_status(gdn_status s, const char* msg);  // gdn_api.cpp

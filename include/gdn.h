@@ -418,8 +418,8 @@ typedef enum gdn_dtype { GDN_DTYPE_F32 = 0, GDN_DTYPE_F16 = 1, GDN_DTYPE_BF16 = 
  *
  * The window's token t is at position kv_start[b] + t. A window's tokens that are
  * not kept need no undoing: the next call's kv_start says where they are overwritten.
- * A needed entry that is not in [0, n_pages), or a position past max_pages *
- * page_size, sets bit 1 of the device error word (gdn_read_device_error); that token is not
+ * A needed entry that is not in [0, n_pages), or a position before 0 (a negative kv_start) or past
+ * max_pages * page_size, sets bit 1 of the device error word (gdn_read_device_error); that token is not
  * written, reads as zeros, and takes no part in the attention.
  */
 size_t gdn_kv4_page_bytes(int kv_heads, int head_dim, int page_size);
@@ -450,7 +450,7 @@ gdn_status gdn_kv4_read(const void* cache, const int32_t* block_table, const int
  *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j),  j = 0 .. kv_start[b] + t,
  *
  * over kv head h / G. Rows at or past seq_len[b] are not written; a row that sees no
- * key (all its pages missing) is zeros.
+ * key (all its pages missing, or its position before 0) is zeros.
  *
  *   q, out    [B][L][T][q_heads][head_dim] (input, output; 16-byte aligned)
  *   workspace at least gdn_kv4_attention_workspace_size() bytes, 16-byte aligned,
