@@ -232,7 +232,8 @@ struct Smem {
     static constexpr uint32_t kOffMul = kOffCol + 2 * kWarps * kCols * 4;  // per column: scale of the raw scores
     static constexpr uint32_t kOffBad = kOffMul + kCols * 4;               // per stage: pages that are not there
     static constexpr uint32_t kOffRed = kOffBad + kWarps * kStages * 4;    // per warp: its stage with its sums, or -1
-    static constexpr uint32_t kBytes = kOffRed + kWarps * 4;
+    static constexpr uint32_t kOffRuns = kOffRed + kWarps * 4;             // maxima and sums of the columns over earlier runs, twice; runs
+    static constexpr uint32_t kBytes = kOffRuns + 2 * 2 * kCols * 4 + 16;
     static_assert(8 * kRedStride * 4 <= Tile<D>::kBytes, "eight columns of sums fit a stage");
 };
 
@@ -246,12 +247,19 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
     constexpr int kTokens = TL::kTokens, kHalfTiles = kTokens / 16;  // m16 tiles of a tile
     constexpr int kRound = kTokens * kWarps;
     constexpr int kMTiles = D / 16;
+    // Sums start afresh every 1024 steps of 16 tokens (65536 tokens of a unit) and are added up with fp32 instructions in the
+    // CTA's part of the workspace: what the tensor cores cut off at every step, and what rounding leaves of a lane's sum of
+    // probabilities, would grow with the row otherwise. Rows of equal values, not split: fp16 outputs over 2^20 keys 2.2e-3
+    // without, 7.4e-4 with (half of fp16's step and the probabilities' are 7.3e-4); fp32 over 2^19 keys 7.7e-5 and 6.8e-6.
+    constexpr int kFreshRounds = 1024 / kHalfTiles;
     constexpr bool kQRegs = NT == 1 && !SPLIT && D <= 128;  // the query fragments stay in registers
     extern __shared__ __align__(128) unsigned char sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     float* col_m = reinterpret_cast<float*>(sm + S::kOffCol);
     float* col_l = col_m + kWarps * kCols;
     float* mul_s = reinterpret_cast<float*>(sm + S::kOffMul);
+    float* runs_s = reinterpret_cast<float*>(sm + S::kOffRuns);
+    int* run_s = reinterpret_cast<int*>(runs_s + 2 * 2 * kCols);
     uint32_t* bad_s = reinterpret_cast<uint32_t*>(sm + S::kOffBad) + warp * kStages;
     int* red_s = reinterpret_cast<int*>(sm + S::kOffRed);
     unsigned char* ring = sm + warp * kStages * TL::kBytes;
@@ -259,7 +267,10 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
     const long long total = all_costs<D>(p.c, lane) * units;
     const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
     JoinRecord* record = reinterpret_cast<JoinRecord*>(p.records) + blockIdx.x;
-    if (tid == 0) *record = JoinRecord{0, 0, 0, 0};
+    if (tid == 0) {
+        *record = JoinRecord{0, 0, 0, 0};
+        *run_s = 0;
+    }
     if (static_cast<int>(blockIdx.x) >= ctas) return;
     long long lo, hi;
     cta_range(total, blockIdx.x, ctas, lo, hi);
@@ -385,6 +396,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
         int r0, r1;
         unit_rounds(cur, r0, r1);
         if (r1 <= r0) break;  // its start alone, at the end of the CTA's places
+        r1 = min(r1, r0 + kFreshRounds);
 
         // --- queries of the unit: B fragments in shared memory, or straight in registers
         const int all_cols = min(x.n * p.group - x.col0, kCols);  // columns that exist (<= 0: none)
@@ -684,8 +696,10 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
             }
         if (lane == 0) red_s[warp] = freed;
         __syncthreads();
-        const bool done = r0 == 0 && r1 == cur.cost - kUnitCost;
-        float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (r0 == 0 ? 1 : 0)) * (kCols * (D + 2));
+        const int run = *run_s;
+        const bool begins = r0 == run * kFreshRounds;  // the unit's first rounds are this CTA's
+        const bool done = begins && r1 == cur.cost - kUnitCost;
+        float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * (kCols * (D + 2));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if (freed >= 0) {
@@ -723,26 +737,45 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
                     const float mw = col_m[w * kCols + c];
                     l += col_l[w * kCols + c] * (mw == -INFINITY ? 0.0f : exp2_approx(mw - mm));
                 }
+                if (run > 0) {  // and the earlier runs
+                    const float* before = runs_s + (run & 1) * 2 * kCols + c;
+                    const float now = mm;
+                    mm = fmaxf(mm, before[0]);
+                    const float f0 = before[0] == -INFINITY ? 0.0f : exp2_approx(before[0] - mm);
+                    const float f1 = now == -INFINITY ? 0.0f : exp2_approx(now - mm);
+                    const float2 y = *reinterpret_cast<const float2*>(slot + c * D + pos);
+                    v = make_float2(y.x * f0 + v.x * f1, y.y * f0 + v.y * f1);
+                    l = before[kCols] * f0 + l * f1;
+                }
                 if (done) {
                     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // no key at all: zeros
                     store_out2(p, q_row(p, b, x, x.col0 + c) + dim_of<D>(pos), v.x * inv, v.y * inv);
                 } else {
                     *reinterpret_cast<float2*>(slot + c * D + pos) = v;
                     if (pos == 0) {
-                        slot[kCols * D + c] = mm;
-                        slot[kCols * D + kCols + c] = l;
+                        float* next = runs_s + ((run & 1) ^ 1) * 2 * kCols + c;  // others may still read this run's
+                        slot[kCols * D + c] = next[0] = mm;
+                        slot[kCols * D + kCols + c] = next[kCols] = l;
                     }
                 }
             }
             __syncthreads();
         }
         if (owed) issue();
-        if (tid == 0 && !done && r0 == 0)  // this CTA's blocks of the join have it
+        const int places = r1 + kUnitCost - cur.at;
+        if (places < cur.left && r1 < cur.cost - kUnitCost) {  // the unit's next run
+            cur.at += places;
+            cur.left -= places;
+            if (tid == 0) *run_s = run + 1;
+            continue;
+        }
+        if (tid == 0 && !done && begins)  // this CTA's blocks of the join have it
             *record = JoinRecord{cur.b, cur.u % p.col_blocks, cur.u / p.col_blocks,
                                  cta_of(total, hi - cur.left - cur.at + cur.cost - 1, ctas) - static_cast<int>(blockIdx.x) + 1};
 
         // --- the next unit
         advance<D>(p.c, units, cur);
+        if (tid == 0) *run_s = 0;
     }
 }
 

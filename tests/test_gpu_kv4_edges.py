@@ -85,6 +85,70 @@ def test_queries_before_the_table_see_nothing(cuda_device, T, Hq, H, D, dtype):
     assert c.g.gdn_read_device_error() == 2
 
 
+@pytest.mark.parametrize("dtype,G,D,keys", [("fp16", 4, 64, 1 << 20), ("fp16", 8, 128, 1 << 20), ("fp16", 16, 64, 1 << 20), ("fp16", 12, 256, 1 << 19),
+                                            ("bf16", 4, 64, 1 << 22), ("fp32", 2, 64, 1 << 19)])
+def test_sums_of_very_long_rows(cuda_device, dtype, G, D, keys):
+    """Single tokens over up to four million keys, values that are all alike in each dimension, and so many sequences that none is
+    split: every output is that value, up to its rounding (or half the type's smallest step), the probabilities' (2^-12,
+    fp32: 2^-22), what matrix instructions cut off (1024 steps of up to 2^-23 each before the sums start afresh), and the
+    fp32 additions that follow: a sum for every 65536 keys, 4 warps', and a lane's 2048 probabilities in each, of
+    either sign (four standard deviations). fp32 calls, which add each step's products with fp32 instructions, have 2 x 1024
+    such roundings instead of cuts. All positions lie in four pages, which every sequence shares."""
+    H, B, page = 16, 57, 256  # 912 units: as many for each CTA, with 456 CTAs or 304
+    c = Cache(cuda_device, 1, 1, H, D, page, 4 * page, spare=0)
+    k = values((1, 1, 4 * page, H, D), dtype, cuda_device, 41)
+    v = values((D,), dtype, cuda_device, 42)
+    c.append(k, v.expand(k.shape).contiguous(), [0])
+    c.t_table = c.t_table.view(1, -1).repeat(B, keys // (4 * page)).contiguous()
+    q = values((B, 1, 1, H * G, D), dtype, cuda_device, 43)
+    out = c.attend(q, [keys - 1] * B).double()
+    assert c.g.gdn_read_device_error() == 0
+    want = torch.from_numpy(O.kv4_dequantise(*O.kv4_quantise(host(v)))).to(cuda_device)
+    info = torch.finfo(TYPES[dtype])
+    cuts = 1024 * 2**-23 if dtype != "fp32" else 4 * 2048 ** 0.5 * 2**-24
+    tolerance = info.eps / 2 + (2**-22 if dtype == "fp32" else 2**-12) + cuts + (keys / 65536 + 8) * 2**-24 + 4 * 2048 ** 0.5 * 2**-24
+    error = (out - want).abs()
+    print("largest error %.2e, %.2f of the tolerance" % ((error / want.abs()).nan_to_num().max().item(),
+                                                         (error / (tolerance * want.abs() + info.smallest_normal * info.eps / 2)).max().item()))
+    assert (error <= tolerance * want.abs() + info.smallest_normal * info.eps / 2).all()
+
+
+@pytest.mark.parametrize("dtype,D", [("fp32", 64), ("fp16", 128), ("bf16", 256), ("fp32", 256)])
+@pytest.mark.parametrize("order", ["rising", "falling", "first missing"])
+def test_very_long_rows_whose_maxima_move(cuda_device, order, dtype, D):
+    """The sums that start afresh and the partial sums of several CTAs meet other maxima than their own: quarters of a row with
+    larger and larger keys, or smaller and smaller, or a row whose first half has no pages. As every page occurs as often as the others, the
+    outputs are those of one of each. Tolerances as in test_sums_of_very_long_rows and, for the scores, in check()."""
+    H, G, B, page, keys = 8, 4, 67, 256, 1 << 18  # 536 units: some for one CTA, some for two
+    c = Cache(cuda_device, 1, 1, H, D, page, 4 * page, spare=0)
+    k, v = (values((1, 1, 4 * page, H, D), dtype, cuda_device, s) for s in (44, 45))
+    k = (k.float() * torch.tensor([0.2, 0.4, 0.7, 1.0], device=cuda_device).repeat_interleave(page).view(1, 1, -1, 1, 1)).to(TYPES[dtype])
+    c.append(k, v, [0])
+    pages = torch.from_numpy(c.table[0].copy()).to(cuda_device)
+    table = (pages.flip(0) if order == "falling" else pages).repeat_interleave(keys // (4 * page))
+    if order == "first missing":
+        table[:table.numel() // 2] = -1
+    c.t_table = table.repeat(B, 1).contiguous()
+    q = values((B, 1, 1, H * G, D), dtype, cuda_device, 46)
+    out = c.attend(q, [keys - 1] * B)
+    assert c.g.gdn_read_device_error() == (2 if order == "first missing" else 0)
+    bytes_, info = c.t_cache.cpu().numpy(), torch.finfo(TYPES[dtype])
+    cuts = 1024 * 2**-23 if dtype != "fp32" else 4 * 2048 ** 0.5 * 2**-24
+    fixed = (2**-22 if dtype == "fp32" else 2**-12) + cuts + (keys / 65536 + 12) * 2**-24 + 4 * 2048 ** 0.5 * 2**-24
+    worst = 0.0
+    for h in range(H):
+        hk, hv = O.kv4_read(bytes_, c.table, 0, 0, h, 4 * page, page, D)
+        if order == "first missing":
+            hk, hv = hk[2 * page:], hv[2 * page:]
+        for i in range(h * G, h * G + G):
+            o, size, qk, s = O.attention_rows(host(q)[:, 0, 0, i], hk, hv, [4 * page] * B, D ** -0.5)
+            rel = fixed + 2 * ((D + 8) * 2.0 ** -24 * qk + 2.0 ** -22 * (2 + s))
+            tol = info.eps / 2 * np.abs(o) + info.smallest_normal * info.eps / 2 + rel * size + 2.0 ** -34 * np.abs(hv).sum(0)
+            worst = max(worst, float((np.abs(host(out)[:, 0, 0, i] - o) / tol).max()))
+    print("largest error %.3f of the tolerance" % worst)
+    assert worst <= 1.0
+
+
 @pytest.mark.parametrize("T,D", [(1, 64), (4, 128), (2, 256), (12, 64), (9, 128), (11, 256)])
 def test_small_probabilities_of_fp32_calls(cuda_device, T, D):
     """Rows that are nearly all one key's, whose value is 0 in half of the dimensions, so that the outputs there are sums of
