@@ -93,7 +93,7 @@ constexpr float kLeastScale = 1.17549435e-38f;  // the factor of raw scores is n
 // 2^(11 - exponent of a row's largest magnitude): scaled by it the row fills fp16's range, exactly.
 __device__ __forceinline__ float row_factor(float a) {
     const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -115), 127);
-    return a > 0.0f && a <= 3.0e38f ? __uint_as_float(static_cast<uint32_t>(138 - e) << 23) : 1.0f;
+    return a > 0.0f && a < INFINITY ? __uint_as_float(static_cast<uint32_t>(138 - e) << 23) : 1.0f;
 }
 
 __device__ __forceinline__ float4 load_q4(const AttnParams& p, size_t i) {

@@ -149,6 +149,21 @@ def test_very_long_rows_whose_maxima_move(cuda_device, order, dtype, D):
     assert worst <= 1.0
 
 
+@pytest.mark.parametrize("T", [1, 20])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_the_largest_finite_queries(cuda_device, dtype, T):
+    """Rows whose largest element is the type's largest, with a scale that brings the scores back."""
+    c = Cache(cuda_device, 1, 1, 2, 64, 16, 70 + T)
+    k, v = (values((1, 1, 70 + T, 2, 64), dtype, cuda_device, s) for s in (4, 5))
+    c.append(k, v, [0])
+    most = torch.finfo(TYPES[dtype]).max
+    q = (values((1, 1, T, 4, 64), "fp32", cuda_device, 6) * 1e37).to(TYPES[dtype])
+    q[..., 3], q[..., 40] = most, -most
+    scale = 2.0 ** -126
+    out = c.attend(q, [70], scale=scale)
+    check(c, 0, q[0, 0], out[0, 0], 70, dtype, scale)
+
+
 @pytest.mark.parametrize("T,D", [(1, 64), (4, 128), (2, 256), (12, 64), (9, 128), (11, 256)])
 def test_small_probabilities_of_fp32_calls(cuda_device, T, D):
     """Rows that are nearly all one key's, whose value is 0 in half of the dimensions, so that the outputs there are sums of
