@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
             a = fmaxf(a, __shfl_xor_sync(~0u, a, 1));
             a = fmaxf(a, __shfl_xor_sync(~0u, a, 2));
             const float f = row_factor(a);
-            col_mul = fmaxf(p.scale_log2 / f, kLeastScale);
+            col_mul = score_factor(p.scale, f);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
                 qr[i] = make_uint2(pack_half2(v[i].x * f, v[i].y * f), pack_half2(v[i].z * f, v[i].w * f));
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
                 const float f = row_factor(a);
-                if (lane == 0) mul_s[c] = fmaxf(p.scale_log2 / f, kLeastScale);
+                if (lane == 0) mul_s[c] = score_factor(p.scale, f);
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
                     if (4 * lane + 128 * i >= D) continue;
@@ -902,7 +902,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t stream) {
     p.q_heads = a.q_heads;
     p.group = a.q_heads / a.c.kv_heads;
     p.dtype = a.dtype;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.scale = a.scale;
     if (on_tensor_cores(a.c.T, p.group)) return launch_kv4_window(p, stream);
     const int nt = column_tiles(a.c.T, p.group);
     p.col_blocks = static_cast<int>((static_cast<long long>(a.c.T) * p.group + 8 * nt - 1) / (8 * nt));

@@ -27,7 +27,7 @@ struct AttnParams {
     float* sums;    // of the window kernel: per CTA the sums of earlier tiles
     int unit_rows, tile_shift;  // of the window kernel: rows of a unit, log2 of a tile's tokens
     DType dtype;
-    float scale_log2;
+    float scale;
 };
 
 // A unit: its layer, kv head, first column, and the positions its columns see.
@@ -94,6 +94,12 @@ constexpr float kLeastScale = 1.17549435e-38f;  // the factor of raw scores is n
 __device__ __forceinline__ float row_factor(float a) {
     const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -115), 127);
     return a > 0.0f && a < INFINITY ? __uint_as_float(static_cast<uint32_t>(138 - e) << 23) : 1.0f;
+}
+
+// Factor of the raw scores of a row that was scaled by f, for exponentials of base 2. The scale is divided first: its
+// product with log2(e) may be out of range where the queries are small.
+__device__ __forceinline__ float score_factor(float scale, float f) {
+    return fmaxf(scale / f * 1.4426950408889634f, kLeastScale);
 }
 
 __device__ __forceinline__ float4 load_q4(const AttnParams& p, size_t i) {

@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
                     const float f = row_factor(a);
-                    if (lane == 0) mul_s[rr] = fmaxf(p.scale_log2 / f, kLeastScale);
+                    if (lane == 0) mul_s[rr] = score_factor(p.scale, f);
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c) {
                         const int d = 4 * lane + 128 * c;

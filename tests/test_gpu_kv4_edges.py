@@ -164,6 +164,21 @@ def test_the_largest_finite_queries(cuda_device, dtype, T):
     check(c, 0, q[0, 0], out[0, 0], 70, dtype, scale)
 
 
+@pytest.mark.parametrize("T", [1, 20])
+def test_the_largest_scale(cuda_device, T):
+    """A scale near the largest number and queries as small: neither overflows on its own."""
+    c = Cache(cuda_device, 1, 1, 2, 64, 16, 70 + T)
+    k, v = (values((1, 1, 70 + T, 2, 64), "fp32", cuda_device, s) for s in (4, 5))
+    c.append(k, v, [0])
+    scale = float(np.float32(3e38))
+    q = values((1, 1, T, 4, 64), "fp32", cuda_device, 6) * 2.0 ** -120
+    out = c.attend(q, [70], scale=2.0 ** 118)
+    check(c, 0, q[0, 0], out[0, 0], 70, "fp32", 2.0 ** 118)
+    q = q * 2.0 ** -10
+    out = c.attend(q, [70], scale=scale)
+    check(c, 0, q[0, 0], out[0, 0], 70, "fp32", scale)
+
+
 @pytest.mark.parametrize("T,D", [(1, 64), (4, 128), (2, 256), (12, 64), (9, 128), (11, 256)])
 def test_small_probabilities_of_fp32_calls(cuda_device, T, D):
     """Rows that are nearly all one key's, whose value is 0 in half of the dimensions, so that the outputs there are sums of
