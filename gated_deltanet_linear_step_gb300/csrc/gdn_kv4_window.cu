@@ -875,8 +875,9 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
         mma_commit(drained);
         (void)wait_for(drained, 0);
     }
-    if (failed && lane == 0) atomicOr(&g_kv4_window_error, kErrWaitTimeout);
     __syncwarp();
+    // (in the issuing warp the elected lane alone knows, whichever it is)
+    if (__any_sync(~0u, failed) && lane == 0) atomicOr(&g_kv4_window_error, kErrWaitTimeout);
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
