@@ -34,7 +34,7 @@
 // scores are set to -inf by a select, and the scales of tokens past the end
 // are set to zero, so whatever such bytes hold (infinities, NaN) does not matter.
 //
-// Work split. A unit is (sequence, layer, kv head, block of query columns), its
+// Work split. A unit is (sequence, layer, kv head) with all its query rows (16 at most: one or two column tiles), its
 // tiles are cut into rounds of one tile per warp, and the rounds of all units are
 // laid end to end and dealt out evenly to the CTAs, whatever the mix of lengths.
 // A unit that crosses a CTA boundary leaves partial sums in the workspace, and a
@@ -160,19 +160,15 @@ __device__ __forceinline__ void advance(const Kv4Cache& c, int units, Cursor& k)
     } while (k.b < c.B && (k.cost = seq_cost<D>(c, k.b)) == 0);
 }
 
-__device__ __forceinline__ Unit unit_of(const AttnParams& p, int b, int u, int columns) {
+__device__ __forceinline__ Unit unit_of(const AttnParams& p, int b, int u) {
     Unit x;
-    const int qb = u % p.col_blocks;
-    const int lh = u / p.col_blocks;
-    x.h = lh % p.c.kv_heads;
-    x.l = lh / p.c.kv_heads;
-    x.col0 = qb * columns;
+    x.h = u % p.c.kv_heads;
+    x.l = u / p.c.kv_heads;
+    x.col0 = 0;
     const Kv4Window w = kv4_window(p.c, b);
     x.start = w.start;
     x.n = w.n;
-    const int t_lo = x.col0 / p.group;
-    const int t_hi = min((x.col0 + columns - 1) / p.group, w.n - 1);
-    x.end = t_lo < w.n ? w.start + min(t_hi + 1, w.cap - w.start) : 0;
+    x.end = w.start + min(w.n, w.cap - w.start);
     return x;
 }
 
@@ -263,7 +259,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
     uint32_t* bad_s = reinterpret_cast<uint32_t*>(sm + S::kOffBad) + warp * kStages;
     int* red_s = reinterpret_cast<int*>(sm + S::kOffRed);
     unsigned char* ring = sm + warp * kStages * TL::kBytes;
-    const int units = p.c.L * p.c.kv_heads * p.col_blocks;
+    const int units = p.c.L * p.c.kv_heads;
     const long long total = all_costs<D>(p.c, lane) * units;
     const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
     JoinRecord* record = reinterpret_cast<JoinRecord*>(p.records) + blockIdx.x;
@@ -299,7 +295,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
                 ready = false;
                 return;
             }
-            const Unit u = unit_of(p, ahead.b, ahead.u, kCols);
+            const Unit u = unit_of(p, ahead.b, ahead.u);
             a_end = u.end;
             a_head = p.c.cache + (static_cast<size_t>(u.l) * p.c.n_pages * p.c.kv_heads + u.h) * head_bytes;
             a_table = p.c.block_table + static_cast<size_t>(ahead.b) * p.c.max_pages;
@@ -391,7 +387,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
     const uint32_t vs_off1 = 2 * TL::kCodeBytes + TL::kScaleBytes + v1 * TL::kBlocks + vs_lane;
 
     while (cur.left > 0) {
-        const Unit x = unit_of(p, cur.b, cur.u, kCols);
+        const Unit x = unit_of(p, cur.b, cur.u);
         const int b = cur.b;
         int r0, r1;
         unit_rounds(cur, r0, r1);
@@ -399,7 +395,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
         r1 = min(r1, r0 + kFreshRounds);
 
         // --- queries of the unit: B fragments in shared memory, or straight in registers
-        const int all_cols = min(x.n * p.group - x.col0, kCols);  // columns that exist (<= 0: none)
+        const int all_cols = x.n * p.group;  // columns that exist
         if (tid == 0 && kv4_runs_out(kv4_window(p.c, b))) atomicOr(&g_kv4_attn_error, kErrBadPage);
         uint2 qr[kQRegs ? D / 16 : 1];
         float col_mul = 0.0f;  // of column g
@@ -410,7 +406,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (g < all_cols) v[i] = load_q4(p, q_row(p, b, x, x.col0 + g) + kSpan * t4 + 4 * i);
+                if (g < all_cols) v[i] = load_q4(p, q_row(p, b, x, g) + kSpan * t4 + 4 * i);
                 a = fmaxf(fmaxf(a, fmaxf(fabsf(v[i].x), fabsf(v[i].y))), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
             }
             a = fmaxf(a, __shfl_xor_sync(~0u, a, 1));
@@ -429,7 +425,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
                     v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (c < all_cols && 4 * lane + 128 * i < D) v[i] = load_q4(p, q_row(p, b, x, x.col0 + c) + 128 * i + 4 * lane);
+                    if (c < all_cols && 4 * lane + 128 * i < D) v[i] = load_q4(p, q_row(p, b, x, c) + 128 * i + 4 * lane);
                     a = fmaxf(fmaxf(a, fmaxf(fabsf(v[i].x), fabsf(v[i].y))), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
                 }
 #pragma unroll
@@ -465,7 +461,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
                 shift[nt][j] = kNone;
                 ls[nt][j] = 0.0f;
                 mul[nt][j] = kQRegs ? __shfl_sync(~0u, col_mul, (c & 7) * 4) : mul_s[c];
-                lim[nt][j] = c < all_cols ? min(x.start + (x.col0 + c) / p.group, x.end - 1) : -1;
+                lim[nt][j] = c < all_cols ? min(x.start + c / p.group, x.end - 1) : -1;
             }
 #pragma unroll
         for (int i = 0; i < kMTiles; ++i)
@@ -474,7 +470,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
         // positions below this are seen by every column that exists (the others' results are not used)
-        const int seen_by_all = min(x.start + x.col0 / p.group + 1, x.end);
+        const int seen_by_all = min(x.start + 1, x.end);
         bool owed = false;  // a consumed stage is not yet refilled
         int freed = -1;     // the last consumed stage
 
@@ -749,7 +745,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
                 }
                 if (done) {
                     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // no key at all: zeros
-                    store_out2(p, q_row(p, b, x, x.col0 + c) + dim_of<D>(pos), v.x * inv, v.y * inv);
+                    store_out2(p, q_row(p, b, x, c) + dim_of<D>(pos), v.x * inv, v.y * inv);
                 } else {
                     *reinterpret_cast<float2*>(slot + c * D + pos) = v;
                     if (pos == 0) {
@@ -770,7 +766,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<D, NT, SPLIT>::kCtas)
             continue;
         }
         if (tid == 0 && !done && begins)  // this CTA's blocks of the join have it
-            *record = JoinRecord{cur.b, cur.u % p.col_blocks, cur.u / p.col_blocks,
+            *record = JoinRecord{cur.b, 0, cur.u,
                                  cta_of(total, hi - cur.left - cur.at + cur.cost - 1, ctas) - static_cast<int>(blockIdx.x) + 1};
 
         // --- the next unit
@@ -792,8 +788,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
     griddep_wait();
     const JoinRecord rec = reinterpret_cast<const JoinRecord*>(p.records)[blockIdx.x];
     if (rec.parts == 0) return;
-    const Unit x = unit_of(p, rec.b, rec.pair * p.col_blocks + rec.block, kCols);
-    if (c >= min(x.n * p.group - x.col0, kCols)) return;
+    const Unit x = unit_of(p, rec.b, rec.pair);
+    if (c >= x.n * p.group) return;
     const int parts = rec.parts;
     const float* base = p.part + static_cast<size_t>(blockIdx.x) * 2 * kSlot;
     auto slot = [&](int i) -> const float* { return i == 0 ? base + kSlot : base + static_cast<size_t>(i) * 2 * kSlot; };
@@ -824,7 +820,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
         l += lsum[w * kPairs + pair];
     }
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    store_out2(p, q_row(p, rec.b, x, x.col0 + c) + dim_of<D>(2 * pair), v.x * inv, v.y * inv);
+    store_out2(p, q_row(p, rec.b, x, c) + dim_of<D>(2 * pair), v.x * inv, v.y * inv);
 }
 
 // Windows of more query rows per kv head than this go to the tensor cores (gdn_kv4_window.cu). 64 sequences of 4096
@@ -905,7 +901,6 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t stream) {
     p.scale = a.scale;
     if (on_tensor_cores(a.c.T, p.group)) return launch_kv4_window(p, stream);
     const int nt = column_tiles(a.c.T, p.group);
-    p.col_blocks = static_cast<int>((static_cast<long long>(a.c.T) * p.group + 8 * nt - 1) / (8 * nt));
     p.records = p.part + static_cast<size_t>(kMaxCtas) * 2 * (8 * nt) * (a.c.head_dim + 2);
     switch (a.c.head_dim) {
         case 64: return launch_dim<64>(p, nt, stream);

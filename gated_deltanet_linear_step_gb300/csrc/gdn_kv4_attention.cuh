@@ -14,7 +14,7 @@ constexpr float kNone = 1e30f;   // the shift of a column that has seen no key
 // The unit, if there is one, whose first rounds a CTA did and whose last ones other CTAs did: what the joining kernel
 // needs to know. `parts` CTAs, this one first, have a partial result of it each.
 struct JoinRecord {
-    int b, block, pair, parts;  // pair: layer and kv head
+    int b, block, pair, parts;  // block: of the window kernel; pair: layer and kv head
 };
 
 struct AttnParams {
@@ -23,14 +23,14 @@ struct AttnParams {
     void* out;
     float* part;    // per CTA two partial results: [columns][D] sums, then maxima and sums of the columns
     void* records;  // per CTA a JoinRecord
-    int q_heads, group, col_blocks;
+    int q_heads, group;
     float* sums;    // of the window kernel: per CTA the sums of earlier tiles
-    int unit_rows, tile_shift;  // of the window kernel: rows of a unit, log2 of a tile's tokens
+    int unit_rows, col_blocks, tile_shift;  // of the window kernel: rows of a unit, units of a window, log2 of a tile's tokens
     DType dtype;
     float scale;
 };
 
-// A unit: its layer, kv head, first column, and the positions its columns see.
+// A unit: its layer, kv head, first column (0 but in the window kernel), and the positions its columns see.
 struct Unit {
     int l, h, col0, start, n, end;  // end: first position that no column sees (not above 0: there is none that one sees)
 };
@@ -132,7 +132,7 @@ __device__ __forceinline__ size_t q_row(const AttnParams& p, int b, const Unit& 
     return (((static_cast<size_t>(b) * p.c.L + x.l) * p.c.T + t) * p.q_heads + head) * p.c.head_dim;
 }
 
-// Windows with many rows, on the tensor cores (gdn_kv4_window.cu); sets p.col_blocks itself.
+// Windows with many rows, on the tensor cores (gdn_kv4_window.cu); sets the fields of its units itself.
 cudaError_t launch_kv4_window(AttnParams p, cudaStream_t stream);
 size_t kv4_window_workspace_bytes(int head_dim);
 

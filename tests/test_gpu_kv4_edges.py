@@ -193,3 +193,22 @@ def test_small_probabilities_of_fp32_calls(cuda_device, T, D):
     start = keys - T
     out = c.attend(q, [start] * B)
     print("largest error %.3f of the tolerance" % max(check(c, b, q[b, 0], out[b, 0], start, "fp32", D ** -0.5) for b in range(B)))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,Hq,H,page", [(1, 16, 2, 16), (8, 1, 1, 64), (4, 4, 2, 32), (9, 2, 2, 16), (3, 6, 2, 128), (1, 9, 1, 32), (1, 32, 2, 16),
+                                         (16, 1, 1, 64), (4, 8, 2, 256)])
+def test_rows_of_the_single_token_kernel(cuda_device, T, Hq, H, page, D, dtype):
+    """Eight, nine and sixteen query rows per kv head: one full column tile, one row of a second, two full ones; as heads, as
+    tokens and as both, windows cut short among them."""
+    start, n = [0, 300, 31, 64], [T, max(T - 1, 1), T, 1]
+    c = Cache(cuda_device, 4, 1, H, D, page, 300 + T)
+    k, v = (values((4, 1, 300 + T, H, D), dtype, cuda_device, s) for s in (61, 62))
+    c.append(k, v, [0] * 4, [s + m for s, m in zip(start, n)])
+    q = values((4, 1, T, Hq, D), dtype, cuda_device, 63)
+    out = c.attend(q, start, n)
+    assert c.g.gdn_read_device_error() == 0
+    for b in range(4):
+        assert out[b, :, n[b]:].isnan().all(), "a row past the window was written"
+        check(c, b, q[b, 0, :n[b]], out[b, 0, :n[b]], start[b], dtype, D ** -0.5)
