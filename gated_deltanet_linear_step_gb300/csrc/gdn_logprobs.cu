@@ -327,12 +327,18 @@ __global__ void __launch_bounds__(kLpThreads, 8) logprobs_kernel(const LogprobAr
         if (tid < kMaxK) best[tid] = 0;
         __syncthreads();
         const int n = count;
-        if (n <= kList) {  // (the list is longer than the CTA has threads)
-            for (int j = tid; j < n; j += kLpThreads) {
+        if (n <= kList) {
+            auto rank = [&](int j) {
                 const unsigned long long me = list[j];
                 int place = 0;
                 for (int i = 0; i < n; ++i) place += list[i] > me;
                 if (place < k) best[place] = me;
+            };
+            if (n <= kLpThreads) {  // nearly always; as one loop: one row of 131072 fp32 7.47 us instead of 7.40
+                if (tid < n) rank(tid);
+            } else {
+#pragma unroll 1
+                for (int j = tid; j < n; j += kLpThreads) rank(j);
             }
         } else {  // many equal values: one exact search per place
             unsigned long long last = ~0ull;
