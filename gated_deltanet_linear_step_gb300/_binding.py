@@ -482,7 +482,8 @@ def gdn_kv4_append(k, v, cache, block_table, kv_start, page_size, seq_len=None, 
     """Quantises the window's keys and values ([B][L][T][kv_heads][head_dim], fp32, fp16 or bf16) into the
     4-bit ``cache`` (uint8 [L][n_pages][gdn_kv4_page_bytes()]): token t of sequence b at position
     ``kv_start[b] + t``, in page ``block_table[b][position // page_size]``. ``block_table`` is int32
-    [B][max_pages]; ``kv_start`` and the optional ``seq_len`` (valid tokens) are int32 [B]."""
+    [B][max_pages]; ``kv_start`` and the optional ``seq_len`` (valid tokens) are int32 [B]. Positions before 0 or past
+    the table, and pages that are not there, are not written and set bit 1 of gdn_read_device_error()."""
     lib = load_library()
     dt, kp, vp = _kv_shape(k, v)
     B, L, T, H, D = k.shape

@@ -26,7 +26,8 @@
 //    (token, next token) pairs of A. The P fragment comes from the S accumulators by movmatrix.
 //
 // Numerics. Queries are scaled by a power of two per row to fill fp16's range
-// (16-bit inputs stay exact; fp32 ones are split into fp16 hi + lo, 22 bits);
+// (16-bit inputs stay exact down to 2^-25 of the row's largest, bf16 ones to 2^-28; fp32 ones are split into fp16 hi + lo, 22
+// bits; fp16's smallest step leaves 2^-36 of the row's largest of any element);
 // scores, maxima, sums and outputs are fp32. Probabilities are rounded to fp16
 // (half a step is 2^-12 of the value, below the 2^-9 of a bf16 output; the reference maximum stands for 2^9, so that small ones
 // keep their bits) or, for fp32, split into hi + lo. Below 2^-23 (hi + lo: 2^-12) of the row's largest they lose bits to fp16's
@@ -44,7 +45,7 @@
 // Each warp fills its own ring of tiles by 16-byte asynchronous copies (four bulk copies of a tile's pieces, each by
 // its own lane, cost more instructions). No warp waits for another but at the joins, and nothing spins.
 //
-// Measured: 64 sequences of 16384 tokens, 8 kv heads of 128, fp16: 204 us, 0.88 of the time that the cache alone takes
+// Measured: 64 sequences of 16384 tokens, 8 kv heads of 128, fp16: 207 us, 0.86 of the time that the cache alone takes
 // at the measured HBM rate; 4 x 131000 tokens, 2 heads of 256: 64 us (0.69); 64 sequences of mixed lengths up to 8192:
 // 42 us (0.49: the start of the kernel, of each unit and the joins take about 15 us); one sequence of 500: 10 us
 // with the joining kernel, a chain of dependent reads (lengths, block table, tile) and the joins.

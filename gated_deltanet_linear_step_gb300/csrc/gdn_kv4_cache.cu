@@ -1,7 +1,7 @@
 // gdn_kv4_cache.cu - writing keys and values into the 4-bit cache and reading
 // them back (the format and the page layout are in gdn_kv4.cuh).
 //
-// Both are one pass over the data and bound by HBM. Writing: one thread per
+// Both are one pass over the data: HBM is the floor. Writing: one thread per
 // block of 16 values, K and V of the same block one after the other, so that
 // both loads are in flight together; consecutive threads take the blocks of a
 // token and then the next token of the same head, so a warp's codes and scales

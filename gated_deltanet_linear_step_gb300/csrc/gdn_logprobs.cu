@@ -21,9 +21,10 @@
 // k of them, can hold one: their elements are read again (from L2, by all threads) and
 // what is >= tau is listed. The list, a little over k long, is ranked by value and
 // then by lowest index; its order of writing does not matter. A list that runs over (many equal
-// values) is replaced by k rounds of an exact search.
+// values) is replaced by k rounds of an exact search, each a pass over the CTA's share. A mask that leaves a CTA's
+// threads fewer than k maxima is such a case: 128 rows of 131072 fp32, k = 20, 498 us with 60 tokens left, 21 us without a mask.
 //
-// Sums are fp32, one per thread over at most a few thousand elements and then
+// Sums are fp32, one per thread over ceil(V / 256 / CTAs of the row) elements (512 for many rows of 131072, 32 for one) and then
 // by trees. x - m is taken before the factor log2(e) of the exponential: scaled by it,
 // a mask of the type's lowest value would overflow, and a row of such masks alone has a distribution.
 

@@ -457,8 +457,10 @@ gdn_status gdn_kv4_read(const void* cache, const int32_t* block_table, const int
  *             owned by the caller; overwritten (partial sums of split sequences)
  *   scale     positive; usually head_dim^-0.5
  *
- * Scores, maxima, sums and the accumulation are fp32. 16-bit queries enter the
- * products exactly, fp32 ones with 22 bits; probabilities are rounded to 11 bits (22 for fp32 calls).
+ * Scores, maxima, sums and the accumulation are fp32. 16-bit queries enter the products exactly, but for elements below
+ * 2^-25 of their row's largest, which may be off by 2^-36 of it; fp32 ones are off by 2^-22 of themselves or 2^-36 of
+ * the row's largest, whichever is more. (Rows whose largest is below 2^-115 lose more.) Probabilities are rounded to 11 bits
+ * (22 for fp32 calls), or by 2^-34 of the row's largest where that is more.
  * The result does not depend on timing, but may differ in its last bits between calls of different sizes.
  */
 size_t gdn_kv4_attention_workspace_size(int B, int L, int T, int q_heads, int kv_heads, int head_dim);
