@@ -10,7 +10,11 @@ namespace gdn {
 
 constexpr float kPShift = 9.0f;  // probabilities are kept relative to 2^-9 of the reference maximum's ...
 constexpr float kSlack = 6.0f;   // ... which is raised when a score exceeds it by 6: none is above 2^15
-constexpr float kNone = 1e30f;   // the shift of a column that has seen no key
+constexpr float kNone = 3.402823466e38f;  // the shift of a column that has seen no key: any finite score is above its negative
+// An exponential's argument is one fused product and sum, s mul + shift, so the largest score's misses 9 by what its product was
+// rounded by when it became the reference maximum. From 2^27 on (in base 2), where fp32 scores are 8 or more apart, that may be more than probabilities have
+// room for: their sum would be 0 or infinite.
+constexpr float kBig = 134217728.0f;
 
 // The unit, if there is one, whose first rounds a CTA did and whose last ones other CTAs did: what the joining kernel
 // needs to know. `parts` CTAs, this one first, have a partial result of it each.
@@ -151,6 +155,41 @@ __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
 }
 
 constexpr float kLeastScale = 1.17549435e-38f;  // the factor of raw scores is never 0: 0 times a masked -inf
+
+__device__ __forceinline__ bool is_big(float m) { return fabsf(m) >= kBig && fabsf(m) < INFINITY; }
+
+// Whether a score exceeds the reference maximum by more than kSlack.
+__device__ __forceinline__ bool is_over(float top, float mul, float shift) { return fmaf(top, mul, shift) > kPShift + kSlack; }
+
+// The factor of the raw scores of a row whose maximum is big, see kBig: a power of two, which rounds nothing, by which the largest one is 2^31 or
+// more and the others are 128 or more below it. The row's softmax is taken as that score alone (and its equals).
+__device__ __forceinline__ float big_factor(float top) {
+    const int e = static_cast<int>(__float_as_uint(fabsf(top)) >> 23) - 127;
+    return __uint_as_float(static_cast<uint32_t>(min(31 - e, 127) + 127) << 23);
+}
+
+// Raises a row's reference maximum m, and with it its shift, to its largest raw score `top`; returns the factor of what was added up before.
+// `first_mul` gives the factor of the row's raw scores, which `mul` is but for rows that are big. (Big rows cost the tensor-core kernels 1 to 2 % of every call:
+// chunks of 1024 tokens after 8000, 318 -> 323 us; done over at the unit's end, as gdn_prompt.cu does it for nothing, 2 to 3 %.)
+template <class F>
+__device__ __forceinline__ float raise(float top, float& m, float& mul, float& shift, F first_mul) {
+    float al = 0.0f;
+    if (__builtin_expect(is_big(m), 0)) {
+        if (!is_over(top, mul, shift)) return 1.0f;
+        mul = first_mul();
+        m = fmaxf(m, top * mul);
+    } else {
+        const float v = fmaxf(m, top * mul);
+        al = v == m ? 1.0f : exp2_approx(m - v);
+        m = v;
+    }
+    shift = m == -INFINITY ? kNone : kPShift - m;
+    if (__builtin_expect(is_big(m), 0)) {
+        mul = big_factor(top);
+        shift = -top * mul;
+    }
+    return al;
+}
 
 // 2^(11 - exponent of a row's largest magnitude): scaled by it the row fills fp16's range, exactly.
 __device__ __forceinline__ float row_factor(float a) {

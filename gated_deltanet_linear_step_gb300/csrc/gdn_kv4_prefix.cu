@@ -477,7 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefix_kernel(const __grid_co
             }
             ++seen;
             const bool some = 32 * quarter < rows;  // this warp has rows
-            const float mul = row < rows ? mul_s[(dual ? kRows * block : 0) + row] : kLeastScale;
+            auto first_mul = [&]() -> float { return row < rows ? mul_s[(dual ? kRows * block : 0) + row] : kLeastScale; };
+            float mul = first_mul();
             float m = -INFINITY, shift = kNone, l = 0.0f, sum_m = -INFINITY;
             float* slot = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (u.r0 == 0 ? 1 : 0)) * (kUnitRows * (D + 2));
             auto four_sums = [&](int c) -> float4& {  // of earlier runs of tiles, of dims c .. c + 3
@@ -536,12 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefix_kernel(const __grid_co
                         __syncwarp();
                         sum_m = m;
                     }
-                    const bool over = fmaf(top, mul, shift) > kPShift + kSlack;
+                    const bool over = is_over(top, mul, shift);
                     if (__any_sync(~0u, over)) {
-                        const float v = over ? fmaxf(m, top * mul) : m;  // (a row's bits do not depend on its neighbours)
-                        const float al = v == m ? 1.0f : exp2_approx(m - v);
-                        m = v;
-                        shift = v == -INFINITY ? kNone : kPShift - v;
+                        const float al = over ? raise(top, m, mul, shift, first_mul) : 1.0f;  // (a row's bits do not depend on its neighbours)
                         l *= al;
                         if (!starts) {  // the sums so far: after the product that is adding to them
                             if (!warp_wait(o_done + 8 * block, static_cast<uint32_t>(m_tiles - 1) & 1u)) {

@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
             asm volatile("bar.sync %0, 256;" ::"r"(1 + 4 * NB + block) : "memory");  // the block's rows have their factors
 
             const bool some = 128 * block + 32 * quarter < rows;  // this warp has rows
-            const float mul = row < rows ? mul_s[row] : kLeastScale;
+            auto first_mul = [&]() -> float { return row < rows ? mul_s[row] : kLeastScale; };
+            float mul = first_mul();
             const int lim = row < rows ? min(x.start + causal(p) * ((x.col0 + row) / p.group), x.end - 1) : -1;
             const int seen_by_all = min(x.start + causal(p) * (x.col0 / p.group) + 1, x.end);
             float m = -INFINITY, shift = kNone, l = 0.0f;
@@ -405,11 +406,8 @@ __global__ void __launch_bounds__(Win<D, SPLIT, NB>::kThreads, Win<D, SPLIT, NB>
                             top = max3(top, max3(t0, s[30], s[31]), t1);
                         }
                         top = fmaxf(top, exchange(top));
-                        if (__any_sync(~0u, fmaf(top, mul, shift) > kPShift + kSlack)) {
-                            const float v = fmaxf(m, top * mul);
-                            const float al = v == m ? 1.0f : exp2_approx(m - v);
-                            m = v;
-                            shift = v == -INFINITY ? kNone : kPShift - v;
+                        if (__any_sync(~0u, is_over(top, mul, shift))) {
+                            const float al = raise(top, m, mul, shift, first_mul);
                             l *= al;
                             if (r > first) {  // this half of the sums so far: after the product that is adding to them
                                 if (!failed && !warp_wait(o_done + 16 * block + 8 * ((n - 1) & 1), tile_parity(n - 1))) failed = true;

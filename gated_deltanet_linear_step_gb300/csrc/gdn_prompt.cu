@@ -228,6 +228,66 @@ __device__ __forceinline__ void take_registers() {
     }
 }
 
+// 16 bytes of a row as floats.
+template <typename T>
+__device__ __forceinline__ void read16(const T* p, float (&x)[16 / sizeof(T)]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const T* v = reinterpret_cast<const T*>(&w);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) x[i] = value_of(v[i]);
+}
+
+// The output of row `last` of the sequence whose rows begin at `first`, by a warp in two passes over its keys: for rows with a reference maximum that
+// is big, see kBig. (Raising their maxima with a factor that changes, as the kernels over the cache do, took 2 to 4 % of every call.)
+template <typename T, int D>
+__device__ __noinline__ void big_row(const PromptArgs& a, int first, int last, int head, int lane) {
+    constexpr int V = 16 / sizeof(T), kMine = D / 32;
+    const int kv_head = head / (a.q_heads / a.kv_heads);
+    const T* q = static_cast<const T*>(a.q) + (static_cast<long long>(first) + last) * a.q_stride + static_cast<long long>(head) * D;
+    const T* k = static_cast<const T*>(a.k) + static_cast<long long>(first) * a.k_stride + static_cast<long long>(kv_head) * D;
+    const T* v = static_cast<const T*>(a.v) + static_cast<long long>(first) * a.v_stride + static_cast<long long>(kv_head) * D;
+    auto score = [&](int key) -> float {
+        if (key > last) return -INFINITY;
+        float s = 0.0f;
+#pragma unroll 2
+        for (int c = 0; c < D; c += V) {
+            float x[V], y[V];
+            read16(q + c, x);
+            read16(k + key * a.k_stride + c, y);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s = fmaf(x[i], y[i], s);
+        }
+        return s;
+    };
+    float top = -INFINITY, l = 0.0f, o[kMine] = {};
+#pragma unroll 1
+    for (int key = 0; key <= last; key += 32) top = fmaxf(top, score(key + lane));
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, i));
+#pragma unroll 1
+    for (int key = 0; key <= last; key += 32) {
+        const float s = score(key + lane), p = exp2_approx((s - top) * a.scale * 1.4426950408889634f);
+        l += p;
+        for (int j = 0; j < 32 && key + j <= last; ++j) {
+            const float f = __shfl_sync(~0u, p, j);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const float y = value_of(v[(key + j) * a.v_stride + kMine * lane + i]);
+                o[i] = finite(y) ? fmaf(f, y, o[i]) : o[i] + y;  // (0 times infinity, where a probability is too small)
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
+    T* out = static_cast<T*>(a.out) + (static_cast<long long>(first) + last) * a.out_stride + static_cast<long long>(head) * D;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        if constexpr (sizeof(T) == 4) out[kMine * lane + i] = o[i] / l;
+        else if constexpr (__is_same(T, __half)) out[kMine * lane + i] = __float2half_rn(o[i] / l);
+        else out[kMine * lane + i] = __float2bfloat16_rn(o[i] / l);
+    }
+}
+
 // ------------------------------------------------------------------ kernel --
 template <typename T, int D>
 __global__ void __launch_bounds__(Prompt<T, D>::kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
@@ -595,7 +655,7 @@ __global__ void __launch_bounds__(Prompt<T, D>::kThreads, 1) prompt_kernel(const
                 unscale = 1.0f / fill_factor(most[1]);
             }
             mul = fmaxf(mul, kLeastScale);
-            float m = -INFINITY, shift = kNone, l = 0.0f, sum_m = -INFINITY;
+            float m = -INFINITY, shift = kNone, l = 0.0f, sum_m = -INFINITY, worst = 0.0f;  // the largest size of m
             auto four_sums = [&](int c) -> float4& {  // of dims c .. c + 3
                 return *reinterpret_cast<float4*>(p.sums + static_cast<size_t>(blockIdx.x) * D * (kBlocks * kRows) + c * (kBlocks * kRows) + 4 * (block * kRows + row));
             };
@@ -666,6 +726,7 @@ __global__ void __launch_bounds__(Prompt<T, D>::kThreads, 1) prompt_kernel(const
                         const float v = over ? fmaxf(m, top * mul) : m;  // (a row's bits do not depend on its neighbours)
                         const float al = v == m ? 1.0f : exp2_approx(m - v);
                         m = v;
+                        worst = fmaxf(worst, v == -INFINITY ? 0.0f : fabsf(v));
                         shift = v == -INFINITY ? kNone : kPShift - v;
                         l *= al;
                         if (!fresh) {  // the sums so far: after the product that is adding to them
@@ -788,6 +849,10 @@ __global__ void __launch_bounds__(Prompt<T, D>::kThreads, 1) prompt_kernel(const
                         }
                     }
                     __syncwarp();
+                    for (unsigned big = __ballot_sync(~0u, valid && worst >= kBig && fabsf(m) < INFINITY); big != 0; big &= big - 1) {
+                        const int r = __ffs(big) - 1;
+                        big_row<T, D>(p.a, x.first, __shfl_sync(~0u, lim, r), __shfl_sync(~0u, x.head0 + row_head, r), lane);
+                    }
                 }
                 tc_fence_before();
             }

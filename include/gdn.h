@@ -461,6 +461,8 @@ gdn_status gdn_kv4_read(const void* cache, const int32_t* block_table, const int
  * 2^-25 of their row's largest, which may be off by 2^-36 of it; fp32 ones are off by 2^-22 of themselves or 2^-36 of
  * the row's largest, whichever is more. (Rows whose largest is below 2^-115 lose more.) Probabilities are rounded to 11 bits
  * (22 for fp32 calls), or by 2^-34 of the row's largest where that is more.
+ * Scores may be as large as fp32 holds (scale times a query's elements too). Where a row's largest is 9e7 or more in size, where fp32 scores
+ * are 4 or more apart, the row is the mean of the values that have that score.
  * The result does not depend on timing, but may differ in its last bits between calls of different sizes.
  */
 size_t gdn_kv4_attention_workspace_size(int B, int L, int T, int q_heads, int kv_heads, int head_dim);
@@ -570,7 +572,7 @@ gdn_status gdn_rope(const void* q, const void* k, void* q_out, void* k_out, cons
  * Rows outside every sequence's valid ones are not written, and what they hold has no effect on others: infinities and NaN in keys or values
  * reach only the rows that see them (in fp32 a row that sees an infinite key may be NaN where the formula is not).
  *
- * Scores and sums are fp32. Probabilities are rounded to the inputs' 16-bit type; fp32 inputs and probabilities enter the products as two
+ * Scores and sums are fp32: q . k and scale q . k may be as large as that holds. Probabilities are rounded to the inputs' 16-bit type; fp32 inputs and probabilities enter the products as two
  * fp16 parts, 22 bits together, down to 2^-40 of the largest of their row (queries) or sequence and head (keys, values).
  */
 size_t gdn_prompt_attention_workspace_size(int B, int n_tokens, int q_heads, int kv_heads, int head_dim, int dtype);
