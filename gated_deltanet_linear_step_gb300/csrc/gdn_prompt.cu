@@ -151,7 +151,10 @@ __device__ __forceinline__ Finder find_all(const PromptArgs& a, int tokens, int 
     }
     for (int b = lane + 32 * kKept; b < a.B; b += 32) most = max(most, blocks_of(a, b, tokens));
     f.levels = __reduce_max_sync(~0u, most);
-    f.total = units_from(a, f, 0, tokens, lane);
+    // borders that fall could make any number of sequences of the same rows: none has units then
+    bool fall = false;
+    for (int b = lane; b < a.B; b += 32) fall = fall || prompt_rows_fall(a, b);
+    f.total = __any_sync(~0u, fall) ? 0 : units_from(a, f, 0, tokens, lane);
     return f;
 }
 

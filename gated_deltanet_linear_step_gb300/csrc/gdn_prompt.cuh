@@ -62,6 +62,11 @@ __device__ __forceinline__ PromptRows prompt_rows(const PromptArgs& a, int b) {
     return r;
 }
 
+// Whether they fall: the sequence may then share rows with others.
+__device__ __forceinline__ bool prompt_rows_fall(const PromptArgs& a, int b) {
+    return min(max(__ldg(a.offsets + b + 1), 0), a.n_tokens) < min(max(__ldg(a.offsets + b), 0), a.n_tokens);
+}
+
 // Whether sequence b's borders fall or lie outside the rows.
 __device__ __forceinline__ bool prompt_borders_bad(const PromptArgs& a, int b) {
     const int lo = __ldg(a.offsets + b), hi = __ldg(a.offsets + b + 1);

@@ -564,7 +564,8 @@ gdn_status gdn_rope(const void* q, const void* k, void* q_out, void* k_out, cons
  *   q, out   [n_tokens][q_heads][head_dim] of a gdn_dtype; k, v [n_tokens][kv_heads][head_dim]. Tokens lie q_stride, k_stride, v_stride and
  *            out_stride elements apart (at least a token's own): the three inputs may be parts of one projection's output. 16-byte aligned,
  *            strides multiples of 16 bytes, below 2^31 elements.
- *   offsets  [B + 1] int32, rising within [0, n_tokens]; others are clamped to that and set bit 2 of the device error word
+ *   offsets  [B + 1] int32, rising within [0, n_tokens]; others are clamped to that and set bit 2 of the device error word. Where they fall
+ *            all the same, no row is written.
  *   seq_len  [B] int32, or NULL: all rows of each
  *   workspace at least gdn_prompt_attention_workspace_size() bytes, 16-byte aligned, owned by the caller; overwritten (NULL if that is 0)
  *   head_dim 64, 128 or 256; scale positive; n_tokens at most GDN_KV4_MAX_T

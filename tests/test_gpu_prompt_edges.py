@@ -56,6 +56,18 @@ def test_prefix_pages_beyond_32_bit_offsets(cuda_device, D):
     del whole
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_borders_that_fall_leave_every_row(cuda_device, dtype):
+    """Falling borders may name the same rows any number of times: the call reports them and does nothing, however many there are."""
+    import gated_deltanet_linear_step_gb300 as g
+
+    q = values((300, 2, 64), dtype, cuda_device, 16)
+    for off in ([30, 20, 64], [0, 300, 0, 300], [0, 300] * 100, [0, 10, 9] + [300] * 200):
+        assert (prompt.attend(q, q, q, off) == 7.0).all() and g.gdn_read_device_error() == 4, off[:4]
+    prompt.check(q, q, q, prompt.attend(q, q, q, [0, 10, 10, 300]), [0, 10, 10, 300], dtype)
+    assert g.gdn_read_device_error() == 0
+
+
 def test_calls_on_two_streams_at_once(cuda_device):
     """Each stream has its own workspaces and outputs; every result has the bits that it has alone."""
     import gated_deltanet_linear_step_gb300 as g
