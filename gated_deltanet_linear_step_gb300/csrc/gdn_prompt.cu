@@ -144,39 +144,59 @@ __device__ __forceinline__ int units_from(const PromptArgs& a, const Finder& f, 
 __device__ __forceinline__ Finder find_all(const PromptArgs& a, int tokens, int lane) {
     Finder f;
     int most = 0;
+    bool fall = false;  // borders that fall could make any number of sequences of the same rows: none has units then
 #pragma unroll
     for (int i = 0; i < kKept; ++i) {
         f.kept[i] = blocks_of(a, lane + 32 * i, tokens);
         most = max(most, f.kept[i]);
+        fall = fall || (lane + 32 * i < a.B && prompt_rows_fall(a, lane + 32 * i));
     }
-    for (int b = lane + 32 * kKept; b < a.B; b += 32) most = max(most, blocks_of(a, b, tokens));
+    for (int b = lane + 32 * kKept; b < a.B; b += 32) {
+        most = max(most, blocks_of(a, b, tokens));
+        fall = fall || prompt_rows_fall(a, b);
+    }
     f.levels = __reduce_max_sync(~0u, most);
-    // borders that fall could make any number of sequences of the same rows: none has units then
-    bool fall = false;
-    for (int b = lane; b < a.B; b += 32) fall = fall || prompt_rows_fall(a, b);
     f.total = __any_sync(~0u, fall) ? 0 : units_from(a, f, 0, tokens, lane);
     return f;
 }
 
-// Sequence and block index of the x-th unit by falling block index.
-__device__ __forceinline__ void find_unit(const PromptArgs& a, const Finder& f, int x, int tokens, int lane, int& seq, int& level) {
-    int lo = 0, hi = f.levels;  // units_from(lo) > x >= units_from(hi)
-    int above = 0;              // units_from(hi)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1, n = units_from(a, f, mid, tokens, lane);
-        if (n > x) {
-            lo = mid;
-        } else {
-            hi = mid;
-            above = n;
+// Where the search for a CTA's units has come to, by falling block index and rising sequence: the units asked for rise, so it goes on from there.
+// (Started afresh for each unit it took longer than the units: 4096 prompts of 1 to 4 tokens 3750 us, now 980.)
+struct Search {
+    int level;   // block index
+    int above;   // units of larger ones
+    int upto;    // and of this one
+    int b0;      // sequences below it ..
+    int before;  // .. have so many units of this block index
+};
+
+// Sequence of the x-th unit, whose block index is then s.level.
+__device__ __forceinline__ int find_unit(const PromptArgs& a, const Finder& f, int x, int tokens, int lane, Search& s) {
+    if (x >= s.upto) {
+        int hi = s.level, above = s.upto, step = 1, lo, upto;  // above: units_from(hi)
+        for (;; step *= 2) {
+            lo = max(hi - step, 0);
+            upto = units_from(a, f, lo, tokens, lane);
+            if (upto > x || lo == 0) break;
+            hi = lo;
+            above = upto;
         }
+        while (hi - lo > 1) {  // units_from(lo) > x >= units_from(hi)
+            const int mid = (lo + hi) >> 1, n = units_from(a, f, mid, tokens, lane);
+            if (n > x) {
+                lo = mid;
+                upto = n;
+            } else {
+                hi = mid;
+                above = n;
+            }
+        }
+        s = Search{lo, above, upto, 0, 0};
     }
-    level = lo;
-    int rank = x - above;
-    seq = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int n = b0 < 32 * kKept ? f.kept[0] : 0;
-        int mine = n;
+    int rank = x - s.above - s.before;
+    for (; s.b0 < a.B; s.b0 += 32) {
+        const int b0 = s.b0;
+        int mine = f.kept[0];
         if (b0 > 0) {
             mine = 0;
 #pragma unroll
@@ -184,16 +204,17 @@ __device__ __forceinline__ void find_unit(const PromptArgs& a, const Finder& f, 
                 if (b0 == 32 * i) mine = f.kept[i];
             if (b0 >= 32 * kKept) mine = blocks_of(a, b0 + lane, tokens);
         }
-        unsigned hit = __ballot_sync(~0u, mine > level);
+        unsigned hit = __ballot_sync(~0u, mine > s.level);
         const int count = __popc(hit);
         if (rank >= count) {
             rank -= count;
+            s.before += count;
             continue;
         }
         for (; rank > 0; --rank) hit &= hit - 1;
-        seq = b0 + __ffs(hit) - 1;
-        return;
+        return b0 + __ffs(hit) - 1;
     }
+    return 0;
 }
 
 // ------------------------------------------------------------------ pieces --
@@ -374,6 +395,7 @@ __global__ void __launch_bounds__(Prompt<T, D>::kThreads, 1) prompt_kernel(const
             // ------------------------------------------------------------- loads
             const int step = kBlocks * p.tokens;
             const Finder f = find_all(p.a, step, lane);
+            Search search{f.levels, 0, 0, 0, 0};
             const int pairs = p.a.kv_heads * p.chunks;
             const long long total = static_cast<long long>(f.total) * pairs;
             int n = 0, u = 0, k_issued = 0, v_issued = 0, q_issued[2] = {0, 0};  // tiles, units; loads, as the elected lane counts them
@@ -387,12 +409,11 @@ __global__ void __launch_bounds__(Prompt<T, D>::kThreads, 1) prompt_kernel(const
                 const long long at = static_cast<long long>(i) * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                 if (at >= total) return x;
                 const int index = static_cast<int>(at / pairs), pair = static_cast<int>(at - static_cast<long long>(index) * pairs);
-                int level;
-                find_unit(p.a, f, index, step, lane, x.seq, level);
+                x.seq = find_unit(p.a, f, index, step, lane, search);
                 const PromptRows r = prompt_rows(p.a, x.seq);
                 x.first = r.first;
                 x.n = r.n;
-                x.token = level * step;
+                x.token = search.level * step;
                 x.kv_head = pair / p.chunks;
                 x.head0 = x.kv_head * (p.a.q_heads / p.a.kv_heads) + (pair - x.kv_head * p.chunks) * p.heads;
 #pragma unroll

@@ -68,6 +68,33 @@ def test_borders_that_fall_leave_every_row(cuda_device, dtype):
     assert g.gdn_read_device_error() == 0
 
 
+def test_thousands_of_short_prompts(cuda_device):
+    """Sequences of 0 to 3 tokens and a longer one among them; four times as many take some four times as long, not sixteen."""
+    import gated_deltanet_linear_step_gb300 as g
+
+    best = {}
+    for B in (5000, 20000):
+        lens = [(7 * i) % 4 for i in range(B)]
+        lens[B // 2] = 700
+        off = prompt.packed(lens)
+        q, k, v = (values((off[-1], h, 64), "bf16", cuda_device, 17 + i) for i, h in enumerate((4, 2, 2)))
+        out = prompt.attend(q, k, v, off)
+        if B == 5000:
+            prompt.check(q, k, v, out, off, "bf16", heads=[1, 2])
+        ws = torch.empty(g.gdn_prompt_attention_workspace_size(B, off[-1], 4, 2, 64, q.dtype), dtype=torch.uint8, device=cuda_device)
+        t_off, times = torch.tensor(off, dtype=torch.int32, device=cuda_device), []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            g.gdn_prompt_attention(q, k, v, t_off, out, ws)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        best[B] = min(times)
+    assert best[20000] < 8 * best[5000], best
+    assert g.gdn_read_device_error() == 0
+
+
 def test_calls_on_two_streams_at_once(cuda_device):
     """Each stream has its own workspaces and outputs; every result has the bits that it has alone."""
     import gated_deltanet_linear_step_gb300 as g
