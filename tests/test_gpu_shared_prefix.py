@@ -138,6 +138,34 @@ def test_a_prefix_longer_than_a_run_of_sums(cuda_device):
         assert worst <= 2.0 ** -11 + 1024 * 2.0 ** -23 + 2400 * 2.0 ** -24, worst
 
 
+@pytest.mark.parametrize("G", [8, 60])  # a unit of up to 128 rows, and one of two blocks
+def test_maxima_that_rise_between_runs_of_sums(cuda_device, G):
+    """60 stretches of 10000 tokens of the prefix, each with one key and one value. A stretch's score is 3 (in base 2) above the one's before it, so the
+    reference maximum is raised every third, and the last CTA of a unit, which has some 40000 (two blocks) or 80000 tokens, starts its sums
+    afresh twice on the way: the earlier ones have to be scaled to the new maximum, and differ in value.
+
+    Keys are exact in the cache: 0.75 a at dim 0 and 0.75 b at dim 16, 16 a + b the number of the stretch. Tolerance, relative (all values are positive): the
+    output's rounding, 2^-12 for each probability's (twice: products and sum), 2^-22 of the largest score (180) for the scale's and the exponential's argument,
+    twice, what matrix instructions cut off of at most 1024 steps of a run, and the fp32 sums of some 2500 probabilities a row and run."""
+    n, B, H, each = 600000, 3, 20, 10000
+    c = Shared(cuda_device, [n], [0, B], B, 1, H, 64, 256, 8)
+    level = [0.5, 6.0, 1.0, 4.0, 1.5, 3.0, 2.0]
+    for s in range(n // each):
+        k = torch.zeros((1, 1, each, H, 64), dtype=torch.float16, device=cuda_device)
+        k[..., 0], k[..., 16] = 0.75 * (s // 16), 0.75 * (s % 16)
+        c.g.gdn_kv4_append(k, torch.full_like(k, level[s % 7]), c.t_cache, c.t_prefix, c.i32([s * each]), 256)
+    own = torch.zeros((B, 1, 8, H, 64), dtype=torch.float16, device=cuda_device)
+    c.g.gdn_kv4_append(own, own, c.t_cache, c.t_own, c.i32([0] * B), 256)
+    q = torch.zeros((B, 1, 1, H * G, 64), dtype=torch.float16, device=cuda_device)
+    q[..., 0], q[..., 16] = 16.0, 1.0
+    out = c.shared(q, [7] * B, scale=4.0 / np.log2(np.e))
+    assert c.g.gdn_read_device_error() == 0
+    w = 2.0 ** (3.0 * (np.arange(n // each) - n // each))
+    want = (w * [level[s % 7] for s in range(n // each)]).sum() / w.sum()
+    worst = float((out.double() - want).abs().max()) / want
+    assert worst <= 2.0 ** -11 + 2 * 2.0 ** -12 + 2 * 2.0 ** -22 * 180 + 1024 * 2.0 ** -23 + 2500 * 2.0 ** -24, worst
+
+
 @pytest.mark.parametrize("dtype,T", [("fp32", 1), ("bf16", 5)])
 def test_what_is_masked_does_not_matter(cuda_device, dtype, T):
     """Bytes of 255 past the prefix, its last page's rest and past the windows; queries that are NaN or infinite."""
