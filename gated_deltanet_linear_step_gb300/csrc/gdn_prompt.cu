@@ -6,8 +6,9 @@
 //   S = Q K^T   128 rows x kTok keys x D,   O += P V   128 rows x D x kTok keys
 //
 // in one pass over the keys with the running reference maximum and sum of a softmax. A row is a (token, query head) pair: a block of 128
-// rows holds the heads of one kv head's group of as many tokens as fit, so that a tile of keys and values serves the whole group. A
-// unit is NB blocks of consecutive tokens; two blocks take turns on the tensor cores, one's softmax beside the other's products.
+// rows holds as many heads of one kv head's group as the largest power of two in the group's size (128 at most), of 128 / heads tokens: a tile of
+// keys and values serves all of a group of 4 or 8, and one head of a group of 5. A unit is NB blocks of consecutive tokens; two blocks take
+// turns on the tensor cores, one's softmax beside the other's products.
 //
 //   warp 0      finds the CTA's units and loads their tiles by TMA
 //   warp 1      issues the products
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(Prompt<T, D>::kThreads, 1) prompt_kernel(const
         PromptUnit x;
         for (int u = 0; !failed && take(u, x, false); ++u) {
             const int tiles = x.tiles[block], token = x.token + block * p.tokens;
-            const bool valid = row_token < p.tokens && token + row_token < x.n;
+            const bool valid = token + row_token < x.n;
             const bool some = __any_sync(~0u, valid);
             const int lim = valid ? token + row_token : -1;
             const long long out_row = static_cast<long long>(x.first) + lim;
@@ -1057,13 +1058,9 @@ bool encode(CUtensorMap* map, const void* p, CUtensorMapDataType type, int dims,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Query heads of a block: the divisor of the group that leaves the fewest of its 128 rows empty, the largest of those (they share keys).
-int block_heads(int group) {
-    int best = 1;
-    for (int h = 1; h <= std::min(group, kRows); ++h)
-        if (group % h == 0 && h * (kRows / h) >= best * (kRows / best)) best = h;
-    return best;
-}
+// Query heads of a block, which share its tiles of keys: as many of the group's as divide it and the 128 rows, so that no row is empty. A group of
+// five or three has one.
+int block_heads(int group) { return std::min(group & -group, kRows); }
 
 // Launches a kernel, `early`: as soon as every CTA of the one before has begun (the three kernels of fp32 calls: 116.7 -> 114.7 us).
 template <class P>
