@@ -6,8 +6,9 @@
 // negative angle (times the same gain): the transpose, which is what gradients need.
 //
 // Angles. A frequency comes as the fraction of a turn per position in 64-bit fixed point, so position x frequency modulo a
-// whole turn is one integer multiplication whatever the position, exact but for the table's own rounding (2^-53 of the
-// frequency). fp32 products of position and frequency would be off by a radian near position 2^24.
+// whole turn is one integer multiplication whatever the position, exact but for the table's own rounding (2^-53 of a turn for each
+// position); the angle is rounded to 2^-28 of a turn when it becomes a float. fp32 products of position and frequency would be off by a radian
+// near position 2^24.
 //
 // What bounds it: HBM, every element read and written once. Persistent CTAs take tokens in turn. A token's rows (whole heads, up to kPiece
 // bytes at a time) come by bulk copies into a ring of stages, turn in place and leave by bulk copies; the cosines and sines of the next token
@@ -64,7 +65,7 @@ struct alignas(sizeof(T) * V) Vec {
     T x[V];
 };
 
-// Cosine and sine of a fraction of a turn, 2^-64 each unit.
+// Cosine and sine of a fraction of a turn, 2^-64 each unit. Its upper 32 bits count; of what is left within an eighth of a turn a float keeps 24 bits.
 __device__ __forceinline__ void turn_cos_sin(uint64_t turn, float& c, float& s) {
     const int hi = static_cast<int>(turn >> 32);
     const int quarter = static_cast<int>((static_cast<uint32_t>(hi) + 0x20000000u) >> 30);

@@ -545,7 +545,8 @@ gdn_status gdn_rope_turns(uint64_t* turns, int rotary_dim, double base, int scal
  *   seq_len    [B] int32, or NULL for T: rows at or past it are not written
  *   head_dim   a multiple of 8 in [8, 512]; rotary_dim even in [2, head_dim]
  *
- * Angles are exact modulo a turn up to 2^-32 of it; products and sums are fp32, rounded once.
+ * Products of position and frequency are exact modulo a turn. An angle is off by the frequency's 2^-53 of a turn for each position (2^-22 of a turn at
+ * the ends of int32) and by its own rounding, 2^-28 of a turn; products and sums are fp32, rounded once.
  */
 #define GDN_ROPE_INTERLEAVED 0x1u
 #define GDN_ROPE_INVERSE 0x2u

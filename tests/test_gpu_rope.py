@@ -9,7 +9,7 @@ import torch
 
 from oracle import operators as O
 from tests.test_gpu_kv4 import TYPES, host, values
-from tests.test_prompt_operators_host import SCALINGS
+from tests.test_prompt_operators_host import SCALINGS, exact_turns
 
 pytestmark = pytest.mark.gpu
 
@@ -82,6 +82,24 @@ def test_far_and_negative_positions(cuda_device, scaling, interleaved):
     for i, p in enumerate(pos):  # exact integer arithmetic for the angle
         f = np.array([((p * x) % 2 ** 64) / 2.0 ** 64 for x in t]) * 2 * np.pi
         check(q[:, :, i:i + 1], out[:, :, i:i + 1], [[1]], f, "fp32", interleaved)
+
+
+@pytest.mark.parametrize("base", [10000.0, 500000.0])
+def test_far_angles_against_exact_ones(cuda_device, base):
+    """Cosine and sine of positions up to the ends of int32 against angles with 50 digits. Tolerance: the table's 2^-53 of a turn for each position, 2^-28 of a
+    turn for the angle's rounding (30 bits to 24) and 2^-32 for its cut, and 2^-22 for cosine, sine and the products with 1 and 0."""
+    import gated_deltanet_linear_step_gb300 as g
+
+    r, pos = 128, [0, 1, -1, 12345, 2 ** 24 + 1, 1000000007, -1234567890, 2 ** 31 - 1, -2 ** 31]
+    x = torch.zeros((1, 1, len(pos), 1, r), device=cuda_device)
+    x[..., :r // 2] = 1.0
+    out = torch.empty_like(x)
+    g.gdn_rope(x, None, g.gdn_rope_turns(r, base=base, device=cuda_device), out, None, positions=torch.tensor([pos], dtype=torch.int32, device=cuda_device))
+    got = host(out)[0, 0, :, 0]
+    for t, p in enumerate(pos):
+        part = np.array([float(p * w % 1) for w in exact_turns(r, base)]) * 2 * np.pi
+        tol = 2 * np.pi * (abs(p) * 2.0 ** -53 + 2.0 ** -28 + 2.0 ** -32) + 2.0 ** -22
+        assert np.abs(got[t, :r // 2] - np.cos(part)).max() <= tol and np.abs(got[t, r // 2:] - np.sin(part)).max() <= tol, p
 
 
 @pytest.mark.parametrize("dtype,r,interleaved", [("bf16", 128, False), ("fp16", 60, False), ("fp32", 128, True)])

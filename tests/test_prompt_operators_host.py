@@ -1,6 +1,8 @@
 """Rotary positions, attention over prompts and over shared prefixes, on the CPU: refusals at the C ABI and in the binding, the table
 of frequencies, and pins of the fp64 restatement."""
 import ctypes
+import math
+from decimal import Decimal, getcontext
 
 import numpy as np
 import pytest
@@ -25,6 +27,39 @@ def test_turns_are_the_frequencies(lib, r, scaling):  # noqa: F811
         want = O.rope_frequencies(r, base, **scaling) / (2 * np.pi)
         assert np.abs(t.astype(np.float64) / 2.0 ** 64 / want - 1).max() < 1e-13 + 2.0 ** -65 / want.min()
         assert (t > 0).all() and (t < 2.0 ** 62).all()
+
+
+def exact_turns(r, base, scaling="none", factor=1.0, original_len=0.0, low=1.0, high=32.0):
+    """Parts of a turn per position with 50 digits."""
+    getcontext().prec = 50
+    atan = lambda n: sum((-1) ** k * Decimal(1) / ((2 * k + 1) * Decimal(n) ** (2 * k + 1)) for k in range(80))  # noqa: E731
+    tau = 2 * (16 * atan(5) - 4 * atan(239))
+    d = Decimal
+    if scaling == "ntk":
+        base = d(base) * (d(factor).ln() * r / (r - 2)).exp()
+    f = [(-d(2 * i) / r * d(base).ln()).exp() for i in range(r // 2)]
+    if scaling == "by_turns":
+        keep = [(d(original_len) * x / tau - d(low)) / (d(high) - d(low)) for x in f]
+    elif scaling == "by_dim":
+        at = [r * (d(original_len) / (tau * d(n))).ln() / (2 * d(base).ln()) for n in (high, low)]
+        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), r - 1)
+        keep = [1 - d(i - lo) / max(d(hi - lo), d("0.001")) for i in range(r // 2)]
+    else:
+        keep = [d(0 if scaling == "linear" else 1)] * len(f)
+    keep = [min(max(x, d(0)), d(1)) for x in keep]
+    return [x * (s + (1 - s) / d(factor)) / tau for x, s in zip(f, keep)]
+
+
+@pytest.mark.parametrize("r", [4, 64, 122, 512])
+@pytest.mark.parametrize("scaling", SCALINGS, ids=lambda s: s["scaling"])
+def test_turns_to_their_last_bits(lib, r, scaling):  # noqa: F811
+    """Within 2^-53 of a turn, as stated: a frequency is at most 0.16 of one, a power is off by some 2^-53 of it times (3 + the power's logarithm), and a blend by a few more."""
+    import gated_deltanet_linear_step_gb300 as g
+
+    for base in (10000.0, 500000.0):
+        t = g.gdn_rope_turns(r, base=base, device="cpu", **scaling).numpy().view(np.uint64)
+        err = [abs(Decimal(int(x)) / 2 ** 64 - w) for x, w in zip(t, exact_turns(r, base, **scaling))]
+        assert max(err) <= Decimal(2) ** -53, float(max(err)) * 2.0 ** 53
 
 
 def test_turns_refuse(lib):  # noqa: F811
