@@ -572,7 +572,8 @@ gdn_status gdn_rope(const void* q, const void* k, void* q_out, void* k_out, cons
  *   head_dim 64, 128 or 256; scale positive; n_tokens at most GDN_KV4_MAX_T
  *
  * Rows outside every sequence's valid ones are not written, and what they hold has no effect on others: infinities and NaN in keys or values
- * reach only the rows that see them (in fp32 a row that sees an infinite key may be NaN where the formula is not).
+ * reach only the rows that see them. (What an infinite value makes infinite may be NaN instead: in fp32, and where its probability is below 2^-34
+ * of the row's largest in fp16 or 2^-126 in bf16. In fp32 a row that sees an infinite key may be NaN where the formula is not.)
  *
  * Scores and sums are fp32: q . k and scale q . k may be as large as that holds. Probabilities are rounded to the inputs' 16-bit type; fp32 inputs and probabilities enter the products as two
  * fp16 parts, 22 bits together, down to 2^-40 of the largest of their row (queries) or sequence and head (keys, values).
